@@ -1,0 +1,127 @@
+/*
+ * flint_attn: attention over the paged key-value cache that flint_qkv_fused
+ * writes, and the upkeep of that cache's pages, for one NVIDIA GB300
+ * (sm_103a).  Part of libflint_moe; the conventions of flint_moe.h hold
+ * (device pointers, caller-owned buffers, a workspace zero-filled once,
+ * synchronous argument errors, no allocation, no host synchronisation).
+ *
+ * Common arguments:
+ *   cache        the paged cache: bf16 keys and values of 128-wide heads.  A
+ *                token at position p of a sequence lives in page
+ *                block_table[b, p / block_size], slot p % block_size; head h
+ *                of it starts at element page * stride_block + slot *
+ *                stride_slot + h * stride_head of k and of v.  k and v are
+ *                16-byte aligned, the strides are multiples of 8 elements.
+ *   block_table  int32 [B, max_blocks], row pitch table_stride elements.
+ *                Entries past a sequence's pages are not read.
+ *   seq_lens     int32 [B]: keys of each sequence, the new tokens' own among
+ *                them (the cache already holds those).  A sequence's keys are
+ *                positions 0 .. seq_lens[b] - 1.
+ *   workspace    its first word is a status word (flint_moe_status reads and
+ *                clears it).  What only the device can see is checked there:
+ *                a length that is negative or past max_blocks * block_size is
+ *                taken as 0 or as that bound, and the keys of a page outside
+ *                [0, num_blocks) are left out; either records
+ *                FLINT_ERR_INVALID_ARG.  Nothing outside the cache is read or
+ *                written.
+ */
+#ifndef FLINT_ATTN_H_
+#define FLINT_ATTN_H_
+
+#include "flint_moe.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+typedef struct {
+  void* k;
+  void* v;
+  long long stride_block, stride_slot, stride_head; /* elements, >= 0, multiples of 8 */
+  long long num_blocks;                             /* pages, 1 .. 2^31 - 1 */
+  int block_size;                                   /* slots of a page, >= 1 */
+  int num_kv_heads;
+} flint_kv_cache;
+
+/* Attention of one new token per sequence (decode).  With G = num_q_heads /
+ * num_kv_heads, query head h reads kv head h / G:
+ *   s_j = scale * (q . k_j), j < seq_lens[b];  lse = log sum_j exp(s_j);
+ *   out = sum_j exp(s_j - lse) v_j.
+ * A sequence of length 0 gets zeros and lse = -inf.
+ *   q      bf16 [B, num_q_heads * 128], row pitch q_stride elements (a
+ *          multiple of 8)
+ *   out    bf16 [B, num_q_heads * 128]
+ *   lse    fp32 [B, num_q_heads] or NULL
+ *   scale  finite, > 0
+ *   workspace  flint_attn_decode_workspace_bytes(B, num_q_heads,
+ *          num_kv_heads) bytes; it serves any B up to that one.
+ * Scores, softmax sums and outputs are accumulated in fp32; the
+ * probabilities enter the second product as the sum of two bf16 values.  The
+ * result does not depend on the order in which the CTAs run.  num_q_heads
+ * must be a multiple of num_kv_heads.  B = 0 is a no-op. */
+size_t flint_attn_decode_workspace_bytes(int B, int num_q_heads, int num_kv_heads);
+int flint_attn_decode(const void* q, long long q_stride, const flint_kv_cache* cache,
+                      const int32_t* block_table, long long table_stride, int max_blocks,
+                      const int32_t* seq_lens, int B, int num_q_heads, float scale, void* out, float* lse,
+                      void* workspace, size_t workspace_bytes, flint_stream_t stream);
+
+/* Attention of whole prompts or of chunks of them, causal, packed: sequence b
+ * owns rows cu_q[b] .. cu_q[b + 1] - 1 of q, its last tokens, so row i of
+ * its n = cu_q[b + 1] - cu_q[b] sees the keys at positions up to
+ * seq_lens[b] - n + i.  A row that sees none (seq_lens[b] < n) gets zeros
+ * and lse = -inf.
+ *   q      bf16 [T, num_q_heads * 128], row pitch q_stride elements (a
+ *          multiple of 8)
+ *   cu_q   int32 [B + 1], not decreasing, from >= 0 up to <= T (a piece that
+ *          breaks this is cut off at T or skipped, and recorded in the status
+ *          word); rows outside cu_q[0] .. cu_q[B] are not written
+ *   out    bf16 [T, num_q_heads * 128],  lse fp32 [T, num_q_heads] or NULL
+ *   workspace  flint_attn_prompt_workspace_bytes(T, B, num_q_heads,
+ *          num_kv_heads) bytes; it serves any T and B up to those.
+ * The other arguments and the formula as for flint_attn_decode.  T = 0 and
+ * B = 0 are no-ops. */
+size_t flint_attn_prompt_workspace_bytes(int T, int B, int num_q_heads, int num_kv_heads);
+int flint_attn_prompt(const void* q, long long q_stride, const flint_kv_cache* cache,
+                      const int32_t* block_table, long long table_stride, int max_blocks, const int32_t* cu_q,
+                      const int32_t* seq_lens, int T, int B, int num_q_heads, float scale, void* out,
+                      float* lse, void* workspace, size_t workspace_bytes, flint_stream_t stream);
+
+/* Copies pages of the cache (all heads, keys and values): for each i < n the
+ * first tokens[i] slots (tokens NULL: all) of page moves[i][0] to page
+ * moves[i][1].  n = num_moves, or the smaller of that and *count (a device
+ * word) when count is given.  A source may occur often (a fork); a
+ * destination must occur once and be no source of the same call.  A pair
+ * with a page outside [0, num_blocks) is skipped, and tokens[i] is cut off to
+ * 0 .. block_size; either records FLINT_ERR_INVALID_ARG in the status word.
+ *   moves      int32 [num_moves, 2]
+ *   workspace  flint_kv_workspace_bytes(cache->num_blocks) bytes
+ * num_moves = 0 is a no-op. */
+int flint_kv_copy_pages(const flint_kv_cache* cache, const int32_t* moves, int num_moves, const int32_t* count,
+                        const int32_t* tokens, void* workspace, size_t workspace_bytes, flint_stream_t stream);
+
+/* Plans the compaction of the cache: the pages that some sequence uses (the
+ * first ceil(seq_lens[b] / block_size) entries of its row; a page shared by
+ * several counts once) move down into pages [0, live), so that the pages from
+ * live on are free.  A sequence is freed by a length of 0.
+ *   new_table  int32 [B, max_blocks] contiguous (output): the renamed pages,
+ *              -1 past each sequence's pages and for a page outside
+ *              [0, num_blocks)
+ *   moves      int32 [num_blocks / 2, 2] (output): pair i takes the i-th used
+ *              page at or above `live` to the i-th unused page below it; -1
+ *              from the last pair on.  No page is both source and destination.
+ *   counts     int32 [2] (output): live, pairs
+ *   workspace  flint_kv_workspace_bytes(num_blocks) bytes
+ * The caches are not touched: flint_kv_copy_pages(cache, moves,
+ * num_blocks / 2, counts + 1, NULL, ...) moves the pages.  new_table may not
+ * overlap block_table.  B = 0 plans an empty pool. */
+size_t flint_kv_workspace_bytes(long long num_blocks);
+int flint_kv_compact_plan(const int32_t* block_table, long long table_stride, int max_blocks,
+                          const int32_t* seq_lens, int B, int block_size, long long num_blocks,
+                          int32_t* new_table, int32_t* moves, int32_t* counts, void* workspace,
+                          size_t workspace_bytes, flint_stream_t stream);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* FLINT_ATTN_H_ */

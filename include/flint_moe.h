@@ -366,8 +366,9 @@ enum {
   FLINT_SPAN_PLAN = 7, FLINT_SPAN_GATHER = 8, FLINT_SPAN_GEMM1 = 9, FLINT_SPAN_GEMM2 = 10,
   FLINT_SPAN_COMBINE = 11, FLINT_SPAN_ADD_NORM = 12, FLINT_SPAN_SHARED_GATE_UP = 13,
   FLINT_SPAN_SHARED_DOWN = 14, FLINT_SPAN_SHARED_ADD = 15, FLINT_SPAN_QKV_GEMV = 16,
-  FLINT_SPAN_QKV_HEADS = 17,
-  FLINT_SPAN_KERNELS = 18, FLINT_SPAN_CTAS = 1024
+  FLINT_SPAN_QKV_HEADS = 17, FLINT_SPAN_ATTN_ROWS = 18, FLINT_SPAN_ATTN_PROMPT = 19,
+  FLINT_SPAN_KV_PLAN = 20, FLINT_SPAN_KV_COPY = 21,
+  FLINT_SPAN_KERNELS = 22, FLINT_SPAN_CTAS = 1024
 };
 int flint_moe_record_spans(unsigned long long* spans);
 

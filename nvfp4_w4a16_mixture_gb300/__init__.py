@@ -16,7 +16,9 @@ from ._lib import (EXPORTED, FLINT_ERR_CUDA, FLINT_ERR_INVALID_ARG, FLINT_ERR_SC
                    flint_moe_workspace_bytes, forward_layer, library_path, load,
                    flint_moe_forward_add_norm, forward_add_norm_layer, flint_moe_record_spans,
                    spans_of, SPAN_NAMES, flint_moe_forward_bf16, flint_moe_forward_nvfp4_shared,
-                   flint_qkv_workspace_bytes, flint_qkv_fused)
+                   flint_qkv_workspace_bytes, flint_qkv_fused, flint_attn_decode_workspace_bytes,
+                   flint_attn_decode, flint_attn_prompt_workspace_bytes, flint_attn_prompt,
+                   flint_kv_workspace_bytes, flint_kv_copy_pages, flint_kv_compact_plan)
 
 __all__ = [
     "EXPORTED", "FLINT_OK", "FLINT_ERR_INVALID_ARG", "FLINT_ERR_UNSUPPORTED",
@@ -26,6 +28,8 @@ __all__ = [
     "flint_moe_prefer_path", "flint_moe_forward_add_norm", "forward_add_norm_layer",
     "flint_moe_record_spans", "spans_of", "SPAN_NAMES", "flint_moe_forward_bf16",
     "flint_moe_forward_nvfp4_shared", "flint_qkv_workspace_bytes", "flint_qkv_fused",
+    "flint_attn_decode_workspace_bytes", "flint_attn_decode", "flint_attn_prompt_workspace_bytes",
+    "flint_attn_prompt", "flint_kv_workspace_bytes", "flint_kv_copy_pages", "flint_kv_compact_plan",
     "FlintMoEError", "alloc_workspace", "flint_moe_debug_fault", "flint_moe_forward",
     "flint_moe_route",
     "flint_moe_route_noalloc", "flint_moe_route_noalloc_bytes",

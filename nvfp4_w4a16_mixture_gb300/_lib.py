@@ -7,6 +7,7 @@ library cannot be built or loaded this module raises: there is no fallback.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import threading
 
@@ -35,7 +36,9 @@ EXPORTED = ("flint_moe_workspace_bytes", "flint_moe_route", "flint_moe_forward",
             "flint_moe_route_noalloc_capacity", "flint_moe_status", "flint_moe_strerror",
             "flint_moe_debug_fault", "flint_moe_plan", "flint_moe_prefer_path",
             "flint_moe_forward_add_norm", "flint_moe_record_spans", "flint_moe_forward_bf16",
-            "flint_moe_forward_nvfp4_shared", "flint_qkv_workspace_bytes", "flint_qkv_fused")
+            "flint_moe_forward_nvfp4_shared", "flint_qkv_workspace_bytes", "flint_qkv_fused",
+            "flint_attn_decode_workspace_bytes", "flint_attn_decode", "flint_attn_prompt_workspace_bytes",
+            "flint_attn_prompt", "flint_kv_workspace_bytes", "flint_kv_copy_pages", "flint_kv_compact_plan")
 
 
 class FlintMoEError(RuntimeError):
@@ -47,6 +50,12 @@ class FlintMoEError(RuntimeError):
 class flint_moe_shape(ctypes.Structure):
     _fields_ = [("M", ctypes.c_int), ("H", ctypes.c_int), ("E", ctypes.c_int),
                 ("top_k", ctypes.c_int), ("I", ctypes.c_int), ("SI", ctypes.c_int)]
+
+
+class flint_kv_cache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("stride_block", ctypes.c_longlong),
+                ("stride_slot", ctypes.c_longlong), ("stride_head", ctypes.c_longlong),
+                ("num_blocks", ctypes.c_longlong), ("block_size", ctypes.c_int), ("num_kv_heads", ctypes.c_int)]
 
 
 _lock = threading.Lock()
@@ -102,6 +111,21 @@ def load() -> ctypes.CDLL:
             lib.flint_qkv_fused.restype = ctypes.c_int
             lib.flint_qkv_fused.argtypes = ([P, P, P, F, P, P, P, P, P, F, P, LL, P, P, P, LL, LL, LL, I, LL, P,
                                              I, I, I, I, I, P, P, P, ctypes.c_size_t, P])
+            C, Z = ctypes.POINTER(flint_kv_cache), ctypes.c_size_t
+            lib.flint_attn_decode_workspace_bytes.restype = Z
+            lib.flint_attn_decode_workspace_bytes.argtypes = [I, I, I]
+            lib.flint_attn_decode.restype = I
+            lib.flint_attn_decode.argtypes = [P, LL, C, P, LL, I, P, I, I, F, P, P, P, Z, P]
+            lib.flint_attn_prompt_workspace_bytes.restype = Z
+            lib.flint_attn_prompt_workspace_bytes.argtypes = [I, I, I, I]
+            lib.flint_attn_prompt.restype = I
+            lib.flint_attn_prompt.argtypes = [P, LL, C, P, LL, I, P, P, I, I, I, F, P, P, P, Z, P]
+            lib.flint_kv_workspace_bytes.restype = Z
+            lib.flint_kv_workspace_bytes.argtypes = [LL]
+            lib.flint_kv_copy_pages.restype = I
+            lib.flint_kv_copy_pages.argtypes = [C, P, I, P, P, P, Z, P]
+            lib.flint_kv_compact_plan.restype = I
+            lib.flint_kv_compact_plan.argtypes = [P, LL, I, P, I, I, LL, P, P, P, P, Z, P]
             _lib = lib
     return _lib
 
@@ -261,8 +285,9 @@ def flint_moe_prefer_path(path: int) -> None:
 
 SPAN_NAMES = ("route", "gate_up", "down", "single_launch", "group_count", "group_scan",
               "group_scatter", "plan", "gather", "gemm1", "gemm2", "combine", "add_norm",
-              "shared_gate_up", "shared_down", "shared_add", "qkv_gemv", "qkv_heads")
-SPAN_KERNELS = 18
+              "shared_gate_up", "shared_down", "shared_add", "qkv_gemv", "qkv_heads", "attn_rows",
+              "attn_prompt", "kv_plan", "kv_copy")
+SPAN_KERNELS = 22
 SPAN_CTAS = 1024
 
 
@@ -386,3 +411,164 @@ def flint_qkv_fused(x, residual, norm_weight, eps: float, weight, weight_scale, 
     if rc != FLINT_OK:
         raise FlintMoEError(rc, "flint_qkv_fused")
     return q_out, residual_out
+
+
+# ------------------------------------------------ the paged cache's operators
+def _want(t, where: str, dtype, *shape, contiguous: bool = True) -> None:
+    """Refuses a tensor of another type, shape (None: any extent), place or,
+    where asked, layout: the kernels would read it as something else."""
+    ok = t.dtype == dtype and t.dim() == len(shape) and all(n is None or n == m for n, m in zip(shape, t.shape))
+    if not ok or t.device.type != "cuda" or (contiguous and not t.is_contiguous()):
+        raise FlintMoEError(FLINT_ERR_INVALID_ARG, where)
+
+
+def _on(stream):
+    """Context in which new tensors belong to `stream`."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream)) if int(stream) else torch.cuda.default_stream()
+    return torch.cuda.stream(stream)
+
+
+def _cache(k_cache, v_cache, where: str) -> flint_kv_cache:
+    for c in (k_cache, v_cache):
+        _want(c, where, torch.bfloat16, None, None, None, 128, contiguous=False)
+    if k_cache.shape != v_cache.shape or k_cache.stride() != v_cache.stride() or k_cache.stride(3) != 1:
+        raise FlintMoEError(FLINT_ERR_INVALID_ARG, where)
+    n, bs, heads, _ = k_cache.shape
+    return flint_kv_cache(_ptr(k_cache), _ptr(v_cache), k_cache.stride(0), k_cache.stride(1), k_cache.stride(2),
+                          n, bs, heads)
+
+
+def flint_attn_decode_workspace_bytes(B: int, num_q_heads: int, num_kv_heads: int) -> int:
+    """Workspace bytes of flint_attn_decode (0 for an invalid shape)."""
+    return int(load().flint_attn_decode_workspace_bytes(int(B), int(num_q_heads), int(num_kv_heads)))
+
+
+def flint_attn_prompt_workspace_bytes(T: int, B: int, num_q_heads: int, num_kv_heads: int) -> int:
+    """Workspace bytes of flint_attn_prompt (0 for an invalid shape)."""
+    return int(load().flint_attn_prompt_workspace_bytes(int(T), int(B), int(num_q_heads), int(num_kv_heads)))
+
+
+def _attention(where, q, k_cache, v_cache, block_table, cu_q, seq_lens, scale, out, lse, workspace, stream):
+    c = _cache(k_cache, v_cache, where)
+    _want(q, where, torch.bfloat16, None, None, contiguous=False)
+    T, width = q.shape
+    nq, B = width // 128, seq_lens.shape[0] if seq_lens.dim() == 1 else -1
+    _want(seq_lens, where, torch.int32, None if cu_q is not None else T)
+    _want(block_table, where, torch.int32, B, None, contiguous=False)
+    if cu_q is not None:
+        _want(cu_q, where, torch.int32, B + 1)
+    if width != nq * 128 or q.stride(1) != 1 or (block_table.shape[1] > 1 and block_table.stride(1) != 1):
+        raise FlintMoEError(FLINT_ERR_INVALID_ARG, where)
+    for t, dtype, n in ((out, torch.bfloat16, width), (lse, torch.float32, nq)):
+        if t is not None:
+            _want(t, where, dtype, T, n)
+    if workspace is not None:
+        _want(workspace, where, torch.uint8, None)
+    with _on(stream):
+        if out is None:
+            out = torch.empty(T, width, dtype=torch.bfloat16, device=q.device)
+        if workspace is None:
+            need = (flint_attn_decode_workspace_bytes(B, nq, c.num_kv_heads) if cu_q is None else
+                    flint_attn_prompt_workspace_bytes(T, B, nq, c.num_kv_heads))
+            workspace = torch.zeros(max(1, need), dtype=torch.uint8, device=q.device)
+    table_stride = block_table.stride(0) if B > 1 else block_table.shape[1]
+    q_stride = q.stride(0) if T > 1 else width
+    scale = float(scale) if scale is not None else 128 ** -0.5
+    common = (_ptr(q), q_stride, ctypes.byref(c), _ptr(block_table), table_stride, block_table.shape[1])
+    rest = (B, nq, scale, _ptr(out), _ptr(lse), _ptr(workspace), workspace.numel(), _stream(stream))
+    if cu_q is None:
+        rc = load().flint_attn_decode(*common, _ptr(seq_lens), *rest)
+    else:
+        rc = load().flint_attn_prompt(*common, _ptr(cu_q), _ptr(seq_lens), T, *rest)
+    if rc != FLINT_OK:
+        raise FlintMoEError(rc, where)
+    return out
+
+
+def flint_attn_decode(q, k_cache, v_cache, block_table, seq_lens, scale=None, out=None, lse=None, workspace=None,
+                      stream=None):
+    """Attention of one new token per sequence over the paged cache: q bf16
+    [B, heads * 128] (any row pitch), k_cache / v_cache bf16 [blocks,
+    block_size, kv_heads, 128] views (any strides but a unit last one),
+    block_table int32 [B, max_blocks], seq_lens int32 [B] (the new token
+    counted).  scale defaults to 128 ** -0.5; lse, when given, is a fp32
+    [B, heads] tensor to fill.  Returns out, bf16 [B, heads * 128].  With no
+    workspace one is allocated and zeroed per call."""
+    return _attention("flint_attn_decode", q, k_cache, v_cache, block_table, None, seq_lens, scale, out, lse,
+                      workspace, stream)
+
+
+def flint_attn_prompt(q, k_cache, v_cache, block_table, cu_q, seq_lens, scale=None, out=None, lse=None,
+                      workspace=None, stream=None):
+    """Causal attention of packed prompts or prompt chunks over the paged
+    cache: q bf16 [T, heads * 128], sequence b's rows cu_q[b] .. cu_q[b + 1]
+    (int32 [B + 1]) being its last tokens of seq_lens[b]; the rest as for
+    flint_attn_decode.  Returns out, bf16 [T, heads * 128]; rows that no
+    sequence owns are not written."""
+    return _attention("flint_attn_prompt", q, k_cache, v_cache, block_table, cu_q, seq_lens, scale, out, lse,
+                      workspace, stream)
+
+
+def flint_kv_workspace_bytes(num_blocks: int) -> int:
+    """Workspace bytes of flint_kv_copy_pages and flint_kv_compact_plan (0 for
+    an invalid pool)."""
+    return int(load().flint_kv_workspace_bytes(int(num_blocks)))
+
+
+def flint_kv_copy_pages(k_cache, v_cache, moves, tokens=None, count=None, workspace=None, stream=None) -> None:
+    """Copies page moves[i, 0] to page moves[i, 1] of both caches (int32
+    [n, 2]); of tokens[i] slots only when tokens (int32 [n]) is given, and of
+    the first count[0] pairs only when count (int32 [1], on the device) is."""
+    where = "flint_kv_copy_pages"
+    c = _cache(k_cache, v_cache, where)
+    _want(moves, where, torch.int32, None, 2)
+    if tokens is not None:
+        _want(tokens, where, torch.int32, moves.shape[0])
+    if count is not None:
+        _want(count, where, torch.int32, 1)
+    with _on(stream):
+        if workspace is None:
+            workspace = torch.zeros(max(1, flint_kv_workspace_bytes(c.num_blocks)), dtype=torch.uint8,
+                                    device=k_cache.device)
+    rc = load().flint_kv_copy_pages(ctypes.byref(c), _ptr(moves), moves.shape[0], _ptr(count), _ptr(tokens),
+                                    _ptr(workspace), workspace.numel(), _stream(stream))
+    if rc != FLINT_OK:
+        raise FlintMoEError(rc, where)
+
+
+def flint_kv_compact_plan(block_table, seq_lens, block_size: int, num_blocks: int, new_table=None, moves=None,
+                          counts=None, workspace=None, stream=None):
+    """Plans the compaction of a pool of num_blocks pages: returns (new_table
+    int32 [B, max_blocks], moves int32 [num_blocks // 2, 2], counts int32 [2] =
+    pages in use, pairs).  flint_kv_copy_pages(k_cache, v_cache, moves,
+    count=counts[1:]) then moves the pages."""
+    where = "flint_kv_compact_plan"
+    _want(seq_lens, where, torch.int32, None)
+    B = seq_lens.shape[0]
+    _want(block_table, where, torch.int32, B, None, contiguous=False)
+    width, pairs = block_table.shape[1], max(0, int(num_blocks)) // 2
+    if width > 1 and block_table.stride(1) != 1:
+        raise FlintMoEError(FLINT_ERR_INVALID_ARG, where)
+    for t, shape in ((new_table, (B, width)), (moves, (pairs, 2)), (counts, (2,))):
+        if t is not None:
+            _want(t, where, torch.int32, *shape)
+    dev = seq_lens.device
+    with _on(stream):
+        if new_table is None:
+            new_table = torch.empty(B, width, dtype=torch.int32, device=dev)
+        if moves is None:
+            moves = torch.empty(pairs, 2, dtype=torch.int32, device=dev)
+        if counts is None:
+            counts = torch.empty(2, dtype=torch.int32, device=dev)
+        if workspace is None:
+            workspace = torch.zeros(max(1, flint_kv_workspace_bytes(num_blocks)), dtype=torch.uint8, device=dev)
+    rc = load().flint_kv_compact_plan(_ptr(block_table), block_table.stride(0) if B > 1 else width, width,
+                                      _ptr(seq_lens), B, int(block_size), int(num_blocks), _ptr(new_table),
+                                      _ptr(moves), _ptr(counts), _ptr(workspace), workspace.numel(),
+                                      _stream(stream))
+    if rc != FLINT_OK:
+        raise FlintMoEError(rc, where)
+    return new_table, moves, counts

@@ -123,7 +123,7 @@ Ws ws_pointers(void* base, const WsLayout& L) {
 static bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 // Streaming multiprocessors of the current device (cached per device).
-static cudaError_t device_sms(int* sms) {
+cudaError_t device_sms(int* sms) {
   static std::atomic<int> cache[64] = {};
   int dev = 0;
   cudaError_t err = cudaGetDevice(&dev);
@@ -380,7 +380,8 @@ int flint_moe_record_spans(unsigned long long* spans) {
                                                      span_buffer_set_fused, span_buffer_set_grouped,
                                                      span_buffer_set_route, span_buffer_set_add_norm,
                                                      span_buffer_set_bf16_experts,
-                                                     span_buffer_set_shared_nvfp4, span_buffer_set_qkv};
+                                                     span_buffer_set_shared_nvfp4, span_buffer_set_qkv,
+                                                     span_buffer_set_attn_rows, span_buffer_set_kv_pages};
   for (auto f : set)
     if (f(spans) != cudaSuccess) return FLINT_ERR_CUDA;
   return FLINT_OK;

@@ -1,0 +1,61 @@
+// What the attention kernels share: the paged cache's addresses, the checks
+// that only the device can make, and the softmax's scalars.
+#pragma once
+
+#include "common.cuh"
+#include "internal.h"
+
+namespace flint {
+
+constexpr int kHeadDim = 128;
+
+// Records an argument error found on the device (the first one wins).
+FLINT_DEV void attn_error(int* status) { atomicCAS(status, 0, FLINT_ERR_INVALID_ARG); }
+
+FLINT_DEV float neg_inf() { return __int_as_float(0xff800000); }
+
+// 2^x by the hardware's approximation (about 2 ulp); 2^-inf = 0.
+FLINT_DEV float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+// Keys of sequence b: its length, taken into [0, max_blocks * block_size].
+FLINT_DEV int seq_keys(const AttnArgs& a, int b) {
+  const int n = ldg_cg_i32(a.seq_lens + b);
+  const long long most = (long long)a.max_blocks * a.block_size;
+  if (n < 0 || n > most) {
+    attn_error(a.status);
+    return n < 0 ? 0 : (int)most;
+  }
+  return n;
+}
+
+// Rows [lo, lo + n) of q that sequence b owns (decode: row b).
+FLINT_DEV void seq_rows(const AttnArgs& a, int b, int& lo, int& n) {
+  if (!a.cu_q) {
+    lo = b;
+    n = 1;
+    return;
+  }
+  const int c0 = ldg_cg_i32(a.cu_q + b), c1 = ldg_cg_i32(a.cu_q + b + 1);
+  lo = c0;
+  n = min(c1, a.T) - c0;
+  if (c0 < 0 || c1 < c0 || c1 > a.T) attn_error(a.status);
+  if (c0 < 0 || n < 0) n = 0;
+}
+
+// Element offset of the key at position pos of sequence b, head 0, or -1 for
+// a page outside the cache.
+FLINT_DEV long long key_offset(const AttnArgs& a, int b, int pos) {
+  const int blk = pos / a.block_size, slot = pos - blk * a.block_size;
+  const int page = ldg_cg_i32(a.block_table + (long long)b * a.table_stride + blk);
+  if (page < 0 || page >= a.num_blocks) {
+    attn_error(a.status);
+    return -1;
+  }
+  return (long long)page * a.s_block + (long long)slot * a.s_slot;
+}
+
+}  // namespace flint

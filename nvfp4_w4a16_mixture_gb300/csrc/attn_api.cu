@@ -1,0 +1,181 @@
+// C-ABI entry points of the paged cache's attention and upkeep (declared in
+// include/flint_attn.h).
+#include <math.h>
+
+#include <cuda_runtime.h>
+
+#include "internal.h"
+
+using namespace flint;
+
+namespace {
+
+bool aligned(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+
+// The widest cache that the kernels' 32-bit key positions and page ids reach.
+constexpr long long kMaxKeys = 1ll << 30;
+
+int check_cache(const flint_kv_cache* c) {
+  if (!c || !c->k || !c->v || !aligned(c->k, 16) || !aligned(c->v, 16)) return FLINT_ERR_INVALID_ARG;
+  if (c->block_size < 1 || c->num_kv_heads < 1 || c->num_blocks < 1) return FLINT_ERR_INVALID_ARG;
+  if (c->num_blocks > 0x7fffffffll) return FLINT_ERR_UNSUPPORTED;
+  const long long s[] = {c->stride_block, c->stride_slot, c->stride_head};
+  for (long long v : s)
+    if (v < 0 || v % 8 != 0) return FLINT_ERR_INVALID_ARG;
+  return FLINT_OK;
+}
+
+int check_table(const int32_t* table, long long stride, int max_blocks, const int32_t* seq_lens, int block_size) {
+  if (max_blocks < 0 || stride < 0) return FLINT_ERR_INVALID_ARG;
+  if ((max_blocks > 0 && !table) || !seq_lens || !aligned(table, 4) || !aligned(seq_lens, 4))
+    return FLINT_ERR_INVALID_ARG;
+  if ((long long)max_blocks * block_size > kMaxKeys) return FLINT_ERR_UNSUPPORTED;
+  return FLINT_OK;
+}
+
+bool heads_ok(int nq, int nkv) { return nq >= 1 && nkv >= 1 && nq <= 65535 && nq % nkv == 0; }
+
+constexpr size_t kStatusBytes = 256;
+
+int attention(bool prompt, const void* q, long long q_stride, const flint_kv_cache* cache,
+              const int32_t* block_table, long long table_stride, int max_blocks, const int32_t* cu_q,
+              const int32_t* seq_lens, int T, int B, int nq, float scale, void* out, float* lse, void* workspace,
+              size_t workspace_bytes, size_t need, flint_stream_t stream) {
+  if (T < 0 || B < 0) return FLINT_ERR_INVALID_ARG;
+  if (!cache || !heads_ok(nq, cache->num_kv_heads)) return FLINT_ERR_INVALID_ARG;
+  if (!(scale > 0.0f) || isinf(scale)) return FLINT_ERR_INVALID_ARG;
+  if (T == 0 || B == 0) return FLINT_OK;
+  int rc = check_cache(cache);
+  if (rc != FLINT_OK) return rc;
+  rc = check_table(block_table, table_stride, max_blocks, seq_lens, cache->block_size);
+  if (rc != FLINT_OK) return rc;
+  if (!q || !out || !aligned(q, 16) || !aligned(out, 16) || !aligned(lse, 4)) return FLINT_ERR_INVALID_ARG;
+  if (q_stride < 0 || q_stride % 8 != 0) return FLINT_ERR_INVALID_ARG;
+  if (prompt && (!cu_q || !aligned(cu_q, 4))) return FLINT_ERR_INVALID_ARG;
+  if ((long long)T * nq > kMaxKeys) return FLINT_ERR_UNSUPPORTED;
+  if (!workspace || !aligned(workspace, 256) || workspace_bytes < need) return FLINT_ERR_WORKSPACE;
+  AttnArgs a = {};
+  a.q = static_cast<const uint16_t*>(q);
+  a.q_stride = q_stride;
+  a.k = static_cast<const uint16_t*>(cache->k);
+  a.v = static_cast<const uint16_t*>(cache->v);
+  a.s_block = cache->stride_block; a.s_slot = cache->stride_slot; a.s_head = cache->stride_head;
+  a.num_blocks = cache->num_blocks;
+  a.block_size = cache->block_size;
+  a.nkv = cache->num_kv_heads;
+  a.nq = nq;
+  a.block_table = block_table;
+  a.table_stride = table_stride;
+  a.max_blocks = max_blocks;
+  a.cu_q = cu_q;
+  a.seq_lens = seq_lens;
+  a.T = T;
+  a.B = B;
+  a.scale = scale;
+  a.out = static_cast<uint16_t*>(out);
+  a.lse = lse;
+  a.status = static_cast<int*>(workspace);
+  return launch_attn_rows(a, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? FLINT_OK : FLINT_ERR_CUDA;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t flint_attn_decode_workspace_bytes(int B, int num_q_heads, int num_kv_heads) {
+  if (B < 0 || !heads_ok(num_q_heads, num_kv_heads)) return 0;
+  return kStatusBytes;
+}
+
+size_t flint_attn_prompt_workspace_bytes(int T, int B, int num_q_heads, int num_kv_heads) {
+  if (T < 0 || B < 0 || !heads_ok(num_q_heads, num_kv_heads)) return 0;
+  return kStatusBytes;
+}
+
+int flint_attn_decode(const void* q, long long q_stride, const flint_kv_cache* cache, const int32_t* block_table,
+                      long long table_stride, int max_blocks, const int32_t* seq_lens, int B, int num_q_heads,
+                      float scale, void* out, float* lse, void* workspace, size_t workspace_bytes,
+                      flint_stream_t stream) {
+  const size_t need = cache ? flint_attn_decode_workspace_bytes(B, num_q_heads, cache->num_kv_heads) : 0;
+  return attention(false, q, q_stride, cache, block_table, table_stride, max_blocks, nullptr, seq_lens, B, B,
+                   num_q_heads, scale, out, lse, workspace, workspace_bytes, need, stream);
+}
+
+int flint_attn_prompt(const void* q, long long q_stride, const flint_kv_cache* cache, const int32_t* block_table,
+                      long long table_stride, int max_blocks, const int32_t* cu_q, const int32_t* seq_lens, int T,
+                      int B, int num_q_heads, float scale, void* out, float* lse, void* workspace,
+                      size_t workspace_bytes, flint_stream_t stream) {
+  const size_t need = cache ? flint_attn_prompt_workspace_bytes(T, B, num_q_heads, cache->num_kv_heads) : 0;
+  return attention(true, q, q_stride, cache, block_table, table_stride, max_blocks, cu_q, seq_lens, T, B,
+                   num_q_heads, scale, out, lse, workspace, workspace_bytes, need, stream);
+}
+
+// Workspace: status word, then one bit per page, then the live pages below
+// each 32-page word.
+static size_t kv_words(long long num_blocks) { return ((size_t)num_blocks + 31) / 32; }
+static size_t kv_bits_bytes(long long num_blocks) { return (kv_words(num_blocks) * 4 + 255) / 256 * 256; }
+
+size_t flint_kv_workspace_bytes(long long num_blocks) {
+  if (num_blocks < 1 || num_blocks > 0x7fffffffll) return 0;
+  return kStatusBytes + 2 * kv_bits_bytes(num_blocks);
+}
+
+int flint_kv_copy_pages(const flint_kv_cache* cache, const int32_t* moves, int num_moves, const int32_t* count,
+                        const int32_t* tokens, void* workspace, size_t workspace_bytes, flint_stream_t stream) {
+  const int rc = check_cache(cache);
+  if (rc != FLINT_OK) return rc;
+  if (num_moves < 0) return FLINT_ERR_INVALID_ARG;
+  if ((long long)cache->block_size * cache->num_kv_heads > kMaxKeys) return FLINT_ERR_UNSUPPORTED;
+  if (num_moves == 0) return FLINT_OK;
+  if (!moves || !aligned(moves, 4) || !aligned(count, 4) || !aligned(tokens, 4)) return FLINT_ERR_INVALID_ARG;
+  if (!workspace || !aligned(workspace, 256) || workspace_bytes < flint_kv_workspace_bytes(cache->num_blocks))
+    return FLINT_ERR_WORKSPACE;
+  KvCopyArgs a = {};
+  a.k = static_cast<uint16_t*>(cache->k);
+  a.v = static_cast<uint16_t*>(cache->v);
+  a.s_block = cache->stride_block; a.s_slot = cache->stride_slot; a.s_head = cache->stride_head;
+  a.num_blocks = cache->num_blocks;
+  a.block_size = cache->block_size;
+  a.nkv = cache->num_kv_heads;
+  a.moves = moves;
+  a.count = count;
+  a.tokens = tokens;
+  a.num_moves = num_moves;
+  a.status = static_cast<int*>(workspace);
+  return launch_kv_copy(a, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? FLINT_OK : FLINT_ERR_CUDA;
+}
+
+int flint_kv_compact_plan(const int32_t* block_table, long long table_stride, int max_blocks,
+                          const int32_t* seq_lens, int B, int block_size, long long num_blocks, int32_t* new_table,
+                          int32_t* moves, int32_t* counts, void* workspace, size_t workspace_bytes,
+                          flint_stream_t stream) {
+  if (B < 0 || block_size < 1 || num_blocks < 1) return FLINT_ERR_INVALID_ARG;
+  if (num_blocks > 0x7fffffffll) return FLINT_ERR_UNSUPPORTED;
+  if (B > 0) {
+    const int rc = check_table(block_table, table_stride, max_blocks, seq_lens, block_size);
+    if (rc != FLINT_OK) return rc;
+    if (max_blocks > 0 && (!new_table || !aligned(new_table, 4))) return FLINT_ERR_INVALID_ARG;
+  }
+  if (!counts || !aligned(counts, 4) || (num_blocks > 1 && (!moves || !aligned(moves, 4))))
+    return FLINT_ERR_INVALID_ARG;
+  if (!workspace || !aligned(workspace, 256) || workspace_bytes < flint_kv_workspace_bytes(num_blocks))
+    return FLINT_ERR_WORKSPACE;
+  uint8_t* wb = static_cast<uint8_t*>(workspace);
+  KvPlanArgs a = {};
+  a.block_table = block_table;
+  a.table_stride = table_stride;
+  a.max_blocks = max_blocks;
+  a.B = B;
+  a.block_size = block_size;
+  a.num_blocks = (int)num_blocks;
+  a.seq_lens = seq_lens;
+  a.new_table = new_table;
+  a.moves = moves;
+  a.counts = counts;
+  a.live = reinterpret_cast<uint32_t*>(wb + kStatusBytes);
+  a.rank = reinterpret_cast<int*>(wb + kStatusBytes + kv_bits_bytes(num_blocks));
+  a.status = reinterpret_cast<int*>(wb);
+  return launch_kv_plan(a, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? FLINT_OK : FLINT_ERR_CUDA;
+}
+
+}  // extern "C"

@@ -5,6 +5,7 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include "flint_attn.h"
 #include "flint_moe.h"
 
 namespace flint {
@@ -161,6 +162,8 @@ cudaError_t span_buffer_set_add_norm(unsigned long long* b);
 cudaError_t span_buffer_set_bf16_experts(unsigned long long* b);
 cudaError_t span_buffer_set_shared_nvfp4(unsigned long long* b);
 cudaError_t span_buffer_set_qkv(unsigned long long* b);
+cudaError_t span_buffer_set_attn_rows(unsigned long long* b);
+cudaError_t span_buffer_set_kv_pages(unsigned long long* b);
 
 // NVFP4 shared expert (shared_nvfp4.cu): sact and ys (workspace), then
 // out = bf16(out + ys) over the block's routed output.
@@ -201,6 +204,56 @@ cudaError_t launch_qkv_fused(const QkvArgs& a, const uint16_t* x, const uint16_t
 cudaError_t launch_bf16_experts(const MoEArgs& a, const uint16_t* w13, const uint16_t* w2,
                                 const uint16_t* shared_out, cudaStream_t st);
 
+// Streaming multiprocessors of the current device (cached per device).
+cudaError_t device_sms(int* sms);
 
+// Attention over the paged cache (attn_rows.cu).  Decode: cu_q is null, T = B
+// and sequence b owns row b.
+struct AttnArgs {
+  const uint16_t* q;  // [T, nq * 128], row pitch q_stride
+  long long q_stride;
+  const uint16_t* k;
+  const uint16_t* v;
+  long long s_block, s_slot, s_head, num_blocks;
+  int block_size, nkv, nq;
+  const int* block_table;
+  long long table_stride;
+  int max_blocks;
+  const int* cu_q;
+  const int* seq_lens;
+  int T, B;
+  float scale;
+  uint16_t* out;  // [T, nq * 128]
+  float* lse;     // [T, nq] or null
+  int* status;
+};
+cudaError_t launch_attn_rows(const AttnArgs& a, cudaStream_t st);
+
+// The cache's pages (kv_pages.cu).
+struct KvCopyArgs {
+  uint16_t* k;
+  uint16_t* v;
+  long long s_block, s_slot, s_head, num_blocks;
+  int block_size, nkv;
+  const int* moves;   // [num_moves, 2]
+  const int* count;   // device word or null
+  const int* tokens;  // [num_moves] or null
+  int num_moves;
+  int* status;
+};
+cudaError_t launch_kv_copy(const KvCopyArgs& a, cudaStream_t st);
+struct KvPlanArgs {
+  const int* block_table;
+  long long table_stride;
+  int max_blocks, B, block_size, num_blocks;
+  const int* seq_lens;
+  int* new_table;
+  int* moves;
+  int* counts;
+  uint32_t* live;  // workspace: one bit per page, all zero between calls
+  int* rank;       // workspace: live pages below each 32-page word
+  int* status;
+};
+cudaError_t launch_kv_plan(const KvPlanArgs& a, cudaStream_t st);
 
 }  // namespace flint

@@ -1,0 +1,406 @@
+"""Attention over the paged cache (flint_attn_decode, flint_attn_prompt):
+refusals (CPU) and parity with float64 (GPU)."""
+from __future__ import annotations
+
+import ctypes
+import math
+
+import pytest
+import torch
+
+import nvfp4_w4a16_mixture_gb300 as fm
+from nvfp4_w4a16_mixture_gb300 import _lib
+from attn_reference import D, LAYOUTS, P_BF16, P_SPLIT, Problem, attention, check
+
+SCALE = D ** -0.5
+FAKE = [0x10000 * (i + 1) for i in range(12)]
+
+
+# ------------------------------------------------------------------ refusals
+def _cache(**kw):
+    f = dict(k=FAKE[0], v=FAKE[1], stride_block=16 * 4 * D, stride_slot=4 * D, stride_head=D, num_blocks=8,
+             block_size=16, num_kv_heads=4)
+    f.update(kw)
+    return _lib.flint_kv_cache(**f)
+
+
+def _call(prompt, cache="own", q=FAKE[2], q_stride=32 * D, table=FAKE[3], tstride=4, width=4, cu=FAKE[4], lens=FAKE[5],
+          T=2, B=2, nq=32, scale=SCALE, out=FAKE[6], lse=None, ws=FAKE[7], ws_bytes=1 << 40):
+    lib = fm.load()
+    c = None if cache is None else ctypes.byref(_cache() if cache == "own" else cache)
+    if prompt:
+        return lib.flint_attn_prompt(q, q_stride, c, table, tstride, width, cu, lens, T, B, nq, scale, out, lse, ws,
+                                     ws_bytes, None)
+    return lib.flint_attn_decode(q, q_stride, c, table, tstride, width, lens, B, nq, scale, out, lse, ws, ws_bytes,
+                                 None)
+
+
+@pytest.mark.parametrize("prompt", [False, True])
+def test_refusals_are_synchronous(prompt):
+    """Every argument error is found before any CUDA call (fake addresses)."""
+    bad = fm.FLINT_ERR_INVALID_ARG
+    for kw in (dict(cache=None), dict(q=None), dict(out=None), dict(lens=None), dict(table=None), dict(B=-1),
+               dict(q=FAKE[2] + 8), dict(out=FAKE[6] + 2), dict(q_stride=32 * D + 4), dict(q_stride=-8),
+               dict(tstride=-1), dict(width=-1), dict(nq=30), dict(nq=0), dict(scale=0.0), dict(scale=-1.0),
+               dict(scale=math.nan), dict(scale=math.inf), dict(lse=FAKE[8] + 2), dict(lens=FAKE[5] + 1),
+               dict(cache=_cache(k=None)), dict(cache=_cache(v=FAKE[1] + 8)), dict(cache=_cache(stride_slot=4 * D + 4)),
+               dict(cache=_cache(stride_head=-D)), dict(cache=_cache(block_size=0)), dict(cache=_cache(num_blocks=0)),
+               dict(cache=_cache(num_kv_heads=0))):
+        assert _call(prompt, **kw) == bad, kw
+    assert _call(prompt, cache=_cache(num_blocks=1 << 31)) == fm.FLINT_ERR_UNSUPPORTED
+    assert _call(prompt, width=1 << 30) == fm.FLINT_ERR_UNSUPPORTED
+    assert _call(prompt, ws=None) == fm.FLINT_ERR_WORKSPACE
+    assert _call(prompt, ws=FAKE[7] + 16) == fm.FLINT_ERR_WORKSPACE
+    assert _call(prompt, ws_bytes=16) == fm.FLINT_ERR_WORKSPACE
+    assert _call(prompt, B=0, T=0, q=None, out=None, ws=None, lens=None, table=None, cu=None) == fm.FLINT_OK
+    if prompt:
+        assert _call(True, cu=None) == bad
+        assert _call(True, T=-1) == bad
+        assert _call(True, T=0, q=None, out=None, ws=None) == fm.FLINT_OK
+
+
+def test_workspace_sizes():
+    assert fm.flint_attn_decode_workspace_bytes(64, 32, 4) > 0
+    assert fm.flint_attn_prompt_workspace_bytes(4096, 8, 32, 4) > 0
+    for n in ((-1, 32, 4), (1, 30, 4), (1, 0, 1), (1, 4, 0)):
+        assert fm.flint_attn_decode_workspace_bytes(*n) == 0
+        assert fm.flint_attn_prompt_workspace_bytes(8, *n) == 0
+    assert fm.flint_attn_prompt_workspace_bytes(-1, 1, 32, 4) == 0
+
+
+def test_binding_refuses_other_types_and_places():
+    """Tensors of another type, shape or place never reach the library."""
+    p = Problem([5], [1], 4, 2, 4)
+    good = dict(q=p.q, k_cache=p.k, v_cache=p.v, block_table=torch.zeros(1, 2, dtype=torch.int32),
+                seq_lens=torch.tensor([5], dtype=torch.int32))
+    for kw in ({}, dict(q=p.q.float()), dict(seq_lens=torch.tensor([5])), dict(k_cache=p.k.half())):
+        with pytest.raises(fm.FlintMoEError) as ei:  # {}: everything on the CPU
+            fm.flint_attn_decode(**{**good, **kw})
+        assert ei.value.code == fm.FLINT_ERR_INVALID_ARG
+
+
+def test_reference_matches_a_direct_softmax():
+    """The float64 reference itself, on one sequence without paging tricks."""
+    p = Problem([7], [3], 2, 1, 16, seed=3)
+    out, lse, _, _ = p.expect(SCALE, 0.0)
+    page = p.table[0][0]
+    k, v = p.k[page, :7, 0].double(), p.v[page, :7, 0].double()
+    for i in range(3):
+        for h in range(2):
+            x = p.q[i, h * D:(h + 1) * D].double()
+            s = (k[:5 + i] @ x) * SCALE
+            assert torch.allclose(out[i, h * D:(h + 1) * D], torch.softmax(s, 0) @ v[:5 + i])
+            assert torch.allclose(lse[i, h], torch.logsumexp(s, 0))
+
+
+# -------------------------------------------------------------------- decode
+def run_decode(p, scale=SCALE, **kw):
+    g = p.gpu()
+    g.pop("cu_q")
+    lse = torch.full((len(p.lens), p.nq), 7.0, dtype=torch.float32, device="cuda")
+    ws = torch.zeros(fm.flint_attn_decode_workspace_bytes(len(p.lens), p.nq, p.nkv), dtype=torch.uint8, device="cuda")
+    out = fm.flint_attn_decode(**g, scale=scale, lse=lse, workspace=ws, **kw)
+    assert fm.flint_moe_status(ws) == fm.FLINT_OK
+    return out, lse
+
+
+DECODE = [
+    # lengths, query heads, kv heads, page
+    ([1], 1, 1, 1),
+    ([1, 0, 2, 15, 16, 17], 32, 4, 16),
+    ([127, 128, 129, 255, 0, 1, 300], 28, 4, 24),
+    ([1000], 8, 1, 16),
+    ([513, 64], 16, 1, 32),
+    ([333], 71, 1, 5),
+    ([40, 700], 24, 8, 3),
+    ([2050, 1], 12, 12, 64),
+    ([5000], 32, 8, 128),
+    ([90] * 70, 4, 2, 16),
+    ([8200, 17, 0, 4100], 40, 8, 256),
+    ([0], 8, 2, 16),
+]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("lens,nq,nkv,page", DECODE)
+def test_decode(lens, nq, nkv, page):
+    p = Problem(lens, [1] * len(lens), nq, nkv, page, seed=len(lens) + nq)
+    out, lse = run_decode(p)
+    check(out, lse, p.expect(SCALE, P_SPLIT), f"decode {lens[:4]}")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("layout", LAYOUTS)
+def test_decode_layouts(layout):
+    p = Problem([77, 300, 5], [1] * 3, 16, 4, 16, layout=layout, seed=5)
+    out, lse = run_decode(p)
+    check(out, lse, p.expect(SCALE, P_SPLIT), layout)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("std,scale", [(12.0, SCALE), (1.5, 1.0), (1.5, 1e-4), (0.0, SCALE)])
+def test_decode_score_ranges(std, scale):
+    """Scores from all equal to spread over hundreds: the running reference
+    moves often, and one key takes nearly all."""
+    p = Problem([700, 33], [1, 1], 16, 2, 16, seed=9, std=std)
+    out, lse = run_decode(p, scale=scale)
+    check(out, lse, p.expect(scale, P_SPLIT), f"std {std} scale {scale}")
+
+
+@pytest.mark.gpu
+def test_decode_rising_scores():
+    """Every key scores above all earlier ones: the reference is raised again
+    and again, in every split and warp."""
+    p = Problem([3000], [1], 8, 1, 16, seed=2)
+    unit = torch.ones(D) / math.sqrt(D)
+    p.q[:] = (unit.repeat(8) * 8).bfloat16()
+    for i in range(3000):
+        p.k[p.table[0][i // 16], i % 16, 0] = (unit * (i * 0.25)).bfloat16()
+    out, lse = run_decode(p)
+    check(out, lse, p.expect(SCALE, P_SPLIT), "rising")
+
+
+@pytest.mark.gpu
+def test_decode_same_bits_again_and_on_another_stream():
+    """The same bits on every run, whatever the CTAs' order, also on a stream
+    of its own with buffers made there, and with a row pitch in q."""
+    p = Problem([4000, 31, 0, 1700], [1] * 4, 32, 4, 16, seed=11)
+    out, lse = run_decode(p)
+    for _ in range(4):
+        again, lse2 = run_decode(p)
+        assert torch.equal(out, again) and torch.equal(lse, lse2)
+    g = p.gpu()
+    g.pop("cu_q")
+    wide = torch.full((4, 32 * D + 64), math.nan, dtype=torch.bfloat16, device="cuda")
+    wide[:, :32 * D] = g["q"]
+    g["q"] = wide[:, :32 * D]
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    other = fm.flint_attn_decode(**g, stream=s)
+    s.synchronize()
+    assert torch.equal(out, other)
+
+
+@pytest.mark.gpu
+def test_decode_in_a_graph():
+    """Captured once, replayed with other lengths in the same buffers."""
+    p = Problem([900, 60], [1, 1], 16, 4, 16, seed=13)
+    g = p.gpu()
+    g.pop("cu_q")
+    ws = torch.zeros(fm.flint_attn_decode_workspace_bytes(2, 16, 4), dtype=torch.uint8, device="cuda")
+    out = torch.empty(2, 16 * D, dtype=torch.bfloat16, device="cuda")
+    fm.flint_attn_decode(**g, out=out, workspace=ws)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        fm.flint_attn_decode(**g, out=out, workspace=ws)
+    for lens in ([900, 60], [1, 0], [433, 59]):
+        g["seq_lens"].copy_(torch.tensor(lens, dtype=torch.int32))
+        graph.replay()
+        torch.cuda.synchronize()
+        want = attention(p.q, p.k, p.v, p.table, p.cu, lens, SCALE, P_SPLIT)
+        check(out, None, want, f"graph {lens}")
+    assert fm.flint_moe_status(ws) == fm.FLINT_OK
+
+
+@pytest.mark.gpu
+def test_decode_bad_pages_and_lengths_are_reported():
+    """A page outside the cache leaves its keys out, a length past the table or
+    below 0 is taken as the bound; each is recorded, and the other sequences
+    are computed as usual."""
+    p = Problem([100, 50, 40], [1] * 3, 8, 2, 16, seed=17)
+    g = p.gpu()
+    g.pop("cu_q")
+    ws = torch.zeros(fm.flint_attn_decode_workspace_bytes(3, 8, 2), dtype=torch.uint8, device="cuda")
+    for bad in (-1, p.blocks, 2 ** 31 - 1):
+        t = g["block_table"].clone()
+        t[0, 2] = bad  # keys 32 .. 47 of sequence 0
+        out = fm.flint_attn_decode(**{**g, "block_table": t}, workspace=ws)
+        assert fm.flint_moe_status(ws) == fm.FLINT_ERR_INVALID_ARG
+        assert fm.flint_moe_status(ws) == fm.FLINT_OK
+        # sequence 0 without that page: the page's keys cut out of its table
+        q = Problem([100, 50, 40], [1] * 3, 8, 2, 16, seed=17)
+        q.table[0] = q.table[0][:2] + q.table[0][3:] + [-7]
+        q.lens = [84, 50, 40]
+        check(out, None, q.expect(SCALE, P_SPLIT), f"page {bad}")
+    whole = Problem([100, 50, 40], [1] * 3, 8, 2, 16, seed=17)
+    want = whole.expect(SCALE, P_SPLIT)
+    g["seq_lens"].copy_(torch.tensor([100, -5, 40], dtype=torch.int32))
+    out = fm.flint_attn_decode(**g, workspace=ws)
+    assert fm.flint_moe_status(ws) == fm.FLINT_ERR_INVALID_ARG
+    assert torch.count_nonzero(out[1]) == 0
+    keep = [0, 2]
+    check(out[keep], None, tuple(w[keep] for w in want), "negative length")
+    # 7 pages of 16 in sequence 0's first entries: a longer length is cut off there
+    g["seq_lens"].copy_(torch.tensor([10 ** 9, 50, 40], dtype=torch.int32))
+    out = fm.flint_attn_decode(**{**g, "block_table": g["block_table"][:, :6].contiguous()}, workspace=ws)
+    assert fm.flint_moe_status(ws) == fm.FLINT_ERR_INVALID_ARG
+    cut = attention(p.q, p.k, p.v, p.table, p.cu, [96, 50, 40], SCALE, P_SPLIT)
+    check(out, None, cut, "length past the table")
+
+
+@pytest.mark.gpu
+def test_decode_inf_and_nan_in_q_stay_in_their_row():
+    """A row of q with a NaN gives a NaN row (as the formula does); the other
+    heads and sequences are untouched."""
+    p = Problem([200, 90], [1, 1], 8, 2, 16, seed=19)
+    want = p.expect(SCALE, P_SPLIT)
+    p.q[0, 3 * D + 5] = math.nan
+    out, lse = run_decode(p)
+    assert torch.isnan(out[0, 3 * D:4 * D]).all() and torch.isnan(lse[0, 3])
+    rows = torch.ones(2, 8, dtype=torch.bool)
+    rows[0, 3] = False
+    cols = rows[:, :, None].expand(2, 8, D).reshape(2, 8 * D)
+    got = out.cpu().double()
+    assert ((got - want[0]).abs() <= want[2])[cols].all()
+
+
+# -------------------------------------------------------------------- prompt
+def run_prompt(p, scale=SCALE, **kw):
+    g = p.gpu()
+    T = p.cu[-1]
+    lse = torch.full((T, p.nq), 7.0, dtype=torch.float32, device="cuda")
+    ws = torch.zeros(fm.flint_attn_prompt_workspace_bytes(T, len(p.lens), p.nq, p.nkv), dtype=torch.uint8,
+                     device="cuda")
+    out = fm.flint_attn_prompt(**g, scale=scale, lse=lse, workspace=ws, **kw)
+    assert fm.flint_moe_status(ws) == fm.FLINT_OK
+    return out, lse
+
+
+PROMPT = [
+    # keys, new rows, query heads, kv heads, page
+    ([1], [1], 1, 1, 1),
+    ([5, 1, 33], [5, 1, 33], 32, 4, 16),
+    ([130], [130], 32, 4, 16),
+    ([300, 257, 1], [300, 257, 1], 28, 4, 24),
+    ([500], [37], 32, 4, 16),
+    ([700, 64, 129], [3, 64, 128], 16, 1, 32),
+    ([260], [260], 71, 1, 5),
+    ([129, 400], [129, 200], 24, 8, 3),
+    ([640], [640], 12, 12, 64),
+    ([513], [513], 8, 1, 128),
+    ([300], [300], 3, 3, 8),
+    ([1025], [1025], 4, 1, 16),
+    ([12, 40, 7], [20, 40, 30], 8, 2, 16),   # fewer keys than rows: the first rows see none
+    ([0, 50, 0], [3, 50, 0], 8, 2, 16),
+    ([2300], [9], 8, 2, 48),
+    ([40, 41, 42, 43] * 10, [40, 41, 42, 43] * 10, 8, 2, 16),
+    ([900, 3], [900, 3], 40, 8, 256),
+]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("lens,qlens,nq,nkv,page", PROMPT)
+def test_prompt(lens, qlens, nq, nkv, page):
+    p = Problem(lens, qlens, nq, nkv, page, seed=sum(lens) + nq)
+    out, lse = run_prompt(p)
+    check(out, lse, p.expect(SCALE, P_BF16), f"prompt {lens[:4]} {qlens[:4]}")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("layout", LAYOUTS)
+def test_prompt_layouts(layout):
+    p = Problem([177, 300, 5], [177, 140, 5], 16, 4, 16, layout=layout, seed=5)
+    out, lse = run_prompt(p)
+    check(out, lse, p.expect(SCALE, P_BF16), layout)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("std,scale", [(12.0, SCALE), (1.5, 1.0), (1.5, 1e-4), (0.0, SCALE)])
+def test_prompt_score_ranges(std, scale):
+    p = Problem([700, 33], [400, 33], 16, 2, 16, seed=9, std=std)
+    out, lse = run_prompt(p, scale=scale)
+    check(out, lse, p.expect(scale, P_BF16), f"std {std} scale {scale}")
+
+
+@pytest.mark.gpu
+def test_prompt_rising_scores():
+    p = Problem([1500], [1500], 8, 1, 16, seed=2)
+    unit = torch.ones(D) / math.sqrt(D)
+    p.q[:] = (unit.repeat(8) * 8).bfloat16()
+    for i in range(1500):
+        p.k[p.table[0][i // 16], i % 16, 0] = (unit * (i * 0.25)).bfloat16()
+    out, lse = run_prompt(p)
+    check(out, lse, p.expect(SCALE, P_BF16), "rising")
+
+
+@pytest.mark.gpu
+def test_prompt_same_bits_again_on_a_stream_and_pitched():
+    p = Problem([700, 31, 3, 900], [700, 31, 3, 500], 32, 4, 16, seed=11)
+    out, lse = run_prompt(p)
+    for _ in range(3):
+        again, lse2 = run_prompt(p)
+        assert torch.equal(out, again) and torch.equal(lse, lse2)
+    g = p.gpu()
+    T = p.cu[-1]
+    wide = torch.full((T, 32 * D + 64), math.nan, dtype=torch.bfloat16, device="cuda")
+    wide[:, :32 * D] = g["q"]
+    g["q"] = wide[:, :32 * D]
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    other = fm.flint_attn_prompt(**g, stream=s)
+    s.synchronize()
+    assert torch.equal(out, other)
+
+
+@pytest.mark.gpu
+def test_prompt_in_a_graph():
+    p = Problem([400, 60], [300, 60], 16, 4, 16, seed=13)
+    g = p.gpu()
+    T = p.cu[-1]
+    ws = torch.zeros(fm.flint_attn_prompt_workspace_bytes(T, 2, 16, 4), dtype=torch.uint8, device="cuda")
+    out = torch.empty(T, 16 * D, dtype=torch.bfloat16, device="cuda")
+    fm.flint_attn_prompt(**g, out=out, workspace=ws)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        fm.flint_attn_prompt(**g, out=out, workspace=ws)
+    for lens, cu in (([400, 60], [0, 300, 360]), ([333, 10], [0, 333, 343]), ([20, 60], [0, 1, 61])):
+        g["seq_lens"].copy_(torch.tensor(lens, dtype=torch.int32))
+        g["cu_q"].copy_(torch.tensor(cu, dtype=torch.int32))
+        out.fill_(3.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        want = attention(p.q, p.k, p.v, p.table, cu, lens, SCALE, P_BF16)
+        n = cu[-1]
+        check(out[:n], None, tuple(w[:n] for w in want), f"graph {lens}")
+        assert bool((out[n:] == 3.0).all()), "rows that no sequence owns are not written"
+    assert fm.flint_moe_status(ws) == fm.FLINT_OK
+
+
+@pytest.mark.gpu
+def test_prompt_bad_pages_and_rows_are_reported():
+    p = Problem([100, 150, 40], [60, 150, 40], 8, 2, 16, seed=17)
+    g = p.gpu()
+    T = p.cu[-1]
+    ws = torch.zeros(fm.flint_attn_prompt_workspace_bytes(T, 3, 8, 2), dtype=torch.uint8, device="cuda")
+    want = p.expect(SCALE, P_BF16)
+    for bad in (-1, p.blocks, 2 ** 31 - 1):
+        t = g["block_table"].clone()
+        t[0, 1] = bad  # keys 16 .. 31 of sequence 0: seen by all its 60 rows (positions 40 ..)
+        out = fm.flint_attn_prompt(**{**g, "block_table": t}, workspace=ws)
+        assert fm.flint_moe_status(ws) == fm.FLINT_ERR_INVALID_ARG
+        assert fm.flint_moe_status(ws) == fm.FLINT_OK
+        q = Problem([100, 150, 40], [60, 150, 40], 8, 2, 16, seed=17)
+        q.table[0] = q.table[0][:1] + q.table[0][2:] + [-7]
+        q.lens = [84, 150, 40]
+        check(out, None, q.expect(SCALE, P_BF16), f"page {bad}")
+    # a piece past T is cut off, one that runs backwards is skipped
+    out = torch.full((T, 8 * D), 3.0, dtype=torch.bfloat16, device="cuda")
+    g["cu_q"].copy_(torch.tensor([0, 60, 210, T + 50], dtype=torch.int32))
+    g["seq_lens"].copy_(torch.tensor([100, 150, 40], dtype=torch.int32))
+    fm.flint_attn_prompt(**g, out=out, workspace=ws)
+    assert fm.flint_moe_status(ws) == fm.FLINT_ERR_INVALID_ARG
+    check(out[:210], None, tuple(w[:210] for w in want), "piece past T")
+    g["cu_q"].copy_(torch.tensor([0, 60, 20, 60], dtype=torch.int32))
+    fm.flint_attn_prompt(**g, workspace=ws)
+    assert fm.flint_moe_status(ws) == fm.FLINT_ERR_INVALID_ARG
+
+
+@pytest.mark.gpu
+def test_decode_and_prompt_agree():
+    """One new token through either entry point."""
+    p = Problem([777, 12], [1, 1], 16, 4, 16, seed=23)
+    a, la = run_decode(p)
+    b, lb = run_prompt(p)
+    want = p.expect(SCALE, P_BF16)
+    check(a, la, want)
+    check(b, lb, want)

@@ -1,0 +1,193 @@
+"""Pages of the paged cache: copies and the compaction plan."""
+from __future__ import annotations
+
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+import nvfp4_w4a16_mixture_gb300 as fm
+from nvfp4_w4a16_mixture_gb300 import _lib
+from attn_reference import D, LAYOUTS, Problem, cache_pair
+
+FAKE = [0x10000 * (i + 1) for i in range(12)]
+
+
+def _cache(**kw):
+    f = dict(k=FAKE[0], v=FAKE[1], stride_block=16 * 4 * D, stride_slot=4 * D, stride_head=D, num_blocks=8,
+             block_size=16, num_kv_heads=4)
+    f.update(kw)
+    return _lib.flint_kv_cache(**f)
+
+
+def test_copy_refusals_are_synchronous():
+    lib = fm.load()
+    need = fm.flint_kv_workspace_bytes(8)
+
+    def call(cache="own", moves=FAKE[2], n=4, count=None, tokens=None, ws=FAKE[3], ws_bytes=need):
+        c = None if cache is None else ctypes.byref(_cache() if cache == "own" else cache)
+        return lib.flint_kv_copy_pages(c, moves, n, count, tokens, ws, ws_bytes, None)
+
+    bad = fm.FLINT_ERR_INVALID_ARG
+    for kw in (dict(cache=None), dict(moves=None), dict(n=-1), dict(moves=FAKE[2] + 2), dict(count=FAKE[4] + 1),
+               dict(tokens=FAKE[4] + 2), dict(cache=_cache(k=FAKE[0] + 8)), dict(cache=_cache(stride_block=12)),
+               dict(cache=_cache(num_blocks=0))):
+        assert call(**kw) == bad, kw
+    assert call(ws=None) == fm.FLINT_ERR_WORKSPACE
+    assert call(ws_bytes=need - 1) == fm.FLINT_ERR_WORKSPACE
+    assert call(n=0, moves=None, ws=None) == fm.FLINT_OK
+
+
+def test_plan_refusals_are_synchronous():
+    lib = fm.load()
+    need = fm.flint_kv_workspace_bytes(100)
+
+    def call(table=FAKE[0], stride=4, width=4, lens=FAKE[1], B=2, bs=16, n=100, new=FAKE[2], moves=FAKE[3],
+             counts=FAKE[4], ws=FAKE[5], ws_bytes=need):
+        return lib.flint_kv_compact_plan(table, stride, width, lens, B, bs, n, new, moves, counts, ws, ws_bytes, None)
+
+    bad = fm.FLINT_ERR_INVALID_ARG
+    for kw in (dict(table=None), dict(lens=None), dict(B=-1), dict(bs=0), dict(n=0), dict(new=None), dict(moves=None),
+               dict(counts=None), dict(stride=-1), dict(width=-1), dict(counts=FAKE[4] + 2)):
+        assert call(**kw) == bad, kw
+    assert call(n=1 << 31) == fm.FLINT_ERR_UNSUPPORTED
+    assert call(ws_bytes=need - 1) == fm.FLINT_ERR_WORKSPACE
+    assert fm.flint_kv_workspace_bytes(0) == 0 and fm.flint_kv_workspace_bytes(1 << 31) == 0
+
+
+# --------------------------------------------------------------------- copies
+def bits(t):
+    return t.contiguous().view(torch.int16).cpu()
+
+
+def filled(blocks, page, nkv, layout, seed):
+    k, v = cache_pair(blocks, page, nkv, layout, 0.0)
+    g = torch.Generator().manual_seed(seed)
+    for c in (k, v):  # any bits, NaNs among them
+        c.copy_(torch.randint(-32768, 32768, c.shape, generator=g, dtype=torch.int32).to(torch.int16).view(torch.bfloat16))
+    if layout == "pairs":
+        both = k._base.cuda()
+        return k, v, both[:, 0], both[:, 1]
+    gk, gv = (c._base.cuda().as_strided(c.shape, c.stride()) if c._base is not None else c.cuda() for c in (k, v))
+    return k, v, gk, gv
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("layout", LAYOUTS)
+@pytest.mark.parametrize("blocks,page,nkv,pairs,partial", [(9, 16, 4, 4, False), (40, 5, 3, 17, True), (3, 1, 1, 1, False),
+                                                           (300, 24, 2, 140, True), (6, 256, 1, 2, True)])
+def test_copy_pages(layout, blocks, page, nkv, pairs, partial):
+    k, v, gk, gv = filled(blocks, page, nkv, layout, seed=blocks)
+    g = torch.Generator().manual_seed(7)
+    order = torch.randperm(blocks, generator=g).tolist()
+    dst = order[:pairs]
+    src = [order[pairs:][i % max(1, (blocks - pairs) // 2)] for i in range(pairs)]  # some sources often
+    tokens = torch.randint(0, page + 1, (pairs,), generator=g, dtype=torch.int32) if partial else None
+    moves = torch.tensor(list(zip(src, dst)), dtype=torch.int32)
+    ws = torch.zeros(fm.flint_kv_workspace_bytes(blocks), dtype=torch.uint8, device="cuda")
+    fm.flint_kv_copy_pages(gk, gv, moves.cuda(), tokens=None if tokens is None else tokens.cuda(), workspace=ws)
+    assert fm.flint_moe_status(ws) == fm.FLINT_OK
+    for i in range(pairs):
+        n = page if tokens is None else int(tokens[i])
+        for c in (k, v):
+            c[dst[i], :n] = c[src[i], :n].clone()
+    assert torch.equal(bits(gk), bits(k)) and torch.equal(bits(gv), bits(v))
+
+
+@pytest.mark.gpu
+def test_copy_pages_count_and_bad_pairs():
+    """Only the first count pairs are copied; a pair outside the cache is
+    skipped, a token count outside the page cut off, and both recorded."""
+    k, v, gk, gv = filled(8, 4, 2, "slots", seed=1)
+    ws = torch.zeros(fm.flint_kv_workspace_bytes(8), dtype=torch.uint8, device="cuda")
+    moves = torch.tensor([[0, 4], [1, 5], [2, 6]], dtype=torch.int32, device="cuda")
+    fm.flint_kv_copy_pages(gk, gv, moves, count=torch.tensor([2], dtype=torch.int32, device="cuda"), workspace=ws)
+    assert fm.flint_moe_status(ws) == fm.FLINT_OK
+    for c in (k, v):
+        c[4], c[5] = c[0].clone(), c[1].clone()
+    assert torch.equal(bits(gk), bits(k)) and torch.equal(bits(gv), bits(v))
+    for count in (0, -3):
+        fm.flint_kv_copy_pages(gk, gv, moves, count=torch.tensor([count], dtype=torch.int32, device="cuda"), workspace=ws)
+    assert torch.equal(bits(gk), bits(k))
+    bad = torch.tensor([[0, 8], [-1, 6], [2, 7], [3, -5]], dtype=torch.int32, device="cuda")
+    fm.flint_kv_copy_pages(gk, gv, bad, workspace=ws)
+    assert fm.flint_moe_status(ws) == fm.FLINT_ERR_INVALID_ARG
+    for c in (k, v):
+        c[7] = c[2].clone()
+    assert torch.equal(bits(gk), bits(k)) and torch.equal(bits(gv), bits(v))
+    tokens = torch.tensor([9, -1], dtype=torch.int32, device="cuda")
+    fm.flint_kv_copy_pages(gk, gv, torch.tensor([[0, 3], [1, 2]], dtype=torch.int32, device="cuda"), tokens=tokens,
+                           workspace=ws)
+    assert fm.flint_moe_status(ws) == fm.FLINT_ERR_INVALID_ARG
+    for c in (k, v):
+        c[3] = c[0].clone()
+    assert torch.equal(bits(gk), bits(k)) and torch.equal(bits(gv), bits(v))
+
+
+# ----------------------------------------------------------------------- plan
+def plan(table, lens, page, blocks):
+    """The plan from its definition, on lists."""
+    need = [-(-n // page) for n in lens]
+    live = sorted({p for row, n in zip(table, need) for p in row[:n]})
+    used = set(live)
+    pairs = list(zip([p for p in live if p >= len(live)], [p for p in range(len(live)) if p not in used]))
+    to = dict(pairs)
+    new = [[to.get(p, p) if i < n else -1 for i, p in enumerate(row)] for row, n in zip(table, need)]
+    return new, pairs + [(-1, -1)] * (blocks // 2 - len(pairs)), [len(live), len(pairs)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("blocks,page,lens,shared", [
+    (1, 16, [3], False), (2, 4, [0, 4], False), (33, 1, [5, 7, 0, 1], False), (64, 16, [200, 17, 333], True),
+    (1000, 16, [1600, 0, 3000, 1], True), (70000, 2, [30001, 17, 60000, 2], False), (40, 8, [320], False),
+    (100, 8, [0, 0], False)])
+def test_compact_plan(blocks, page, lens, shared):
+    g = torch.Generator().manual_seed(blocks)
+    need = [-(-n // page) for n in lens]
+    order = torch.randperm(blocks, generator=g).tolist()
+    width, at, table = max(need) + 1, 0, []
+    for i, n in enumerate(need):
+        row = order[at:at + n]
+        at += n
+        if shared and i:
+            m = min(n, need[0]) // 2
+            row[:m] = table[0][:m]  # a common prefix
+        table.append(row + [5 * blocks] * (width - n))
+    ws = torch.zeros(fm.flint_kv_workspace_bytes(blocks), dtype=torch.uint8, device="cuda")
+    t, n = torch.tensor(table, dtype=torch.int32, device="cuda"), torch.tensor(lens, dtype=torch.int32, device="cuda")
+    want = plan(table, lens, page, blocks)
+    for _ in range(2):  # the workspace serves the next call
+        new, moves, counts = fm.flint_kv_compact_plan(t, n, page, blocks, workspace=ws)
+        assert fm.flint_moe_status(ws) == fm.FLINT_OK
+        assert counts.tolist() == want[2]
+        assert np.array_equal(moves.cpu().numpy(), np.array(want[1], dtype=np.int32).reshape(-1, 2))
+        assert new.tolist() == want[0]
+
+
+@pytest.mark.gpu
+def test_compact_plan_bad_pages():
+    t = torch.tensor([[3, 99, 1], [-4, 5, 7]], dtype=torch.int32, device="cuda")
+    n = torch.tensor([12, -1], dtype=torch.int32, device="cuda")
+    ws = torch.zeros(fm.flint_kv_workspace_bytes(10), dtype=torch.uint8, device="cuda")
+    new, moves, counts = fm.flint_kv_compact_plan(t, n, 4, 10, workspace=ws)
+    assert fm.flint_moe_status(ws) == fm.FLINT_ERR_INVALID_ARG
+    assert counts.tolist() == [2, 1] and moves[0].tolist() == [3, 0]
+    assert new.tolist() == [[0, -1, 1], [-1, -1, -1]]
+
+
+@pytest.mark.gpu
+def test_compacted_cache_answers_the_same():
+    """Attention before and after a compaction: the same bits."""
+    p = Problem([100, 0, 333, 57], [1] * 4, 16, 4, 16, seed=31, spare=60)
+    g = p.gpu()
+    g.pop("cu_q")
+    before = fm.flint_attn_decode(**g)
+    new, moves, counts = fm.flint_kv_compact_plan(g["block_table"], g["seq_lens"], p.page, p.blocks)
+    fm.flint_kv_copy_pages(g["k_cache"], g["v_cache"], moves, count=counts[1:])
+    live = int(counts[0])
+    assert live == sum(-(-n // 16) for n in p.lens) and int(new.max()) < live
+    g["k_cache"][live:] = float("nan")  # free
+    g["v_cache"][live:] = float("nan")
+    after = fm.flint_attn_decode(**{**g, "block_table": new})
+    assert torch.equal(before, after)
