@@ -381,7 +381,8 @@ int flint_moe_record_spans(unsigned long long* spans) {
                                                      span_buffer_set_route, span_buffer_set_add_norm,
                                                      span_buffer_set_bf16_experts,
                                                      span_buffer_set_shared_nvfp4, span_buffer_set_qkv,
-                                                     span_buffer_set_attn_rows, span_buffer_set_kv_pages};
+                                                     span_buffer_set_attn_rows, span_buffer_set_kv_pages,
+                                                     span_buffer_set_attn_prompt};
   for (auto f : set)
     if (f(spans) != cudaSuccess) return FLINT_ERR_CUDA;
   return FLINT_OK;

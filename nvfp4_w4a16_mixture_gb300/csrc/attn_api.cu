@@ -75,7 +75,11 @@ int attention(bool prompt, const void* q, long long q_stride, const flint_kv_cac
   a.out = static_cast<uint16_t*>(out);
   a.lse = lse;
   a.status = static_cast<int*>(workspace);
-  return launch_attn_rows(a, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? FLINT_OK : FLINT_ERR_CUDA;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  const cudaError_t err = prompt && attn_prompt_supported(a)
+                              ? launch_attn_prompt(a, prompt_ws(workspace, T, B, nq, a.nkv), st)
+                              : launch_attn_rows(a, st);
+  return err == cudaSuccess ? FLINT_OK : FLINT_ERR_CUDA;
 }
 
 }  // namespace
@@ -89,7 +93,7 @@ size_t flint_attn_decode_workspace_bytes(int B, int num_q_heads, int num_kv_head
 
 size_t flint_attn_prompt_workspace_bytes(int T, int B, int num_q_heads, int num_kv_heads) {
   if (T < 0 || B < 0 || !heads_ok(num_q_heads, num_kv_heads)) return 0;
-  return kStatusBytes;
+  return prompt_ws(nullptr, T, B, num_q_heads, num_kv_heads).total;
 }
 
 int flint_attn_decode(const void* q, long long q_stride, const flint_kv_cache* cache, const int32_t* block_table,

@@ -229,6 +229,24 @@ struct AttnArgs {
 };
 cudaError_t launch_attn_rows(const AttnArgs& a, cudaStream_t st);
 
+// Prompt attention on tcgen05 (attn_prompt.cu): its plan and the partial
+// results of units that several CTAs share, in the workspace.
+constexpr int kPromptCtas = 152;  // most CTAs of its grid (one per SM)
+struct PromptWs {
+  int* count;            // [2 * kPromptCtas]: finished parts of a shared unit, zero between calls
+  int4* starts;          // [kPromptCtas + 1]: each CTA's first unit
+  long long* head;       // [2]: total weight, CTAs at work
+  int* first;            // [B + 1]: first entry of each sequence
+  int4* entries;         // [entries, 2]
+  long long* prefix;     // [entries + 1]: weight before each entry
+  float* parts;          // [2 * kPromptCtas] slots
+  size_t total;
+};
+PromptWs prompt_ws(void* base, int T, int B, int nq, int nkv);
+bool attn_prompt_supported(const AttnArgs& a);
+cudaError_t launch_attn_prompt(const AttnArgs& a, const PromptWs& w, cudaStream_t st);
+cudaError_t span_buffer_set_attn_prompt(unsigned long long* b);
+
 // The cache's pages (kv_pages.cu).
 struct KvCopyArgs {
   uint16_t* k;
