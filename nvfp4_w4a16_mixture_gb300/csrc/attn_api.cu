@@ -78,7 +78,7 @@ int attention(bool prompt, const void* q, long long q_stride, const flint_kv_cac
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const cudaError_t err = prompt && attn_prompt_supported(a)
                               ? launch_attn_prompt(a, prompt_ws(workspace, T, B, nq, a.nkv), st)
-                              : launch_attn_rows(a, st);
+                              : launch_attn_rows(a, rows_ws(workspace), st);
   return err == cudaSuccess ? FLINT_OK : FLINT_ERR_CUDA;
 }
 
@@ -88,12 +88,13 @@ extern "C" {
 
 size_t flint_attn_decode_workspace_bytes(int B, int num_q_heads, int num_kv_heads) {
   if (B < 0 || !heads_ok(num_q_heads, num_kv_heads)) return 0;
-  return kStatusBytes;
+  return rows_ws(nullptr).total;
 }
 
 size_t flint_attn_prompt_workspace_bytes(int T, int B, int num_q_heads, int num_kv_heads) {
   if (T < 0 || B < 0 || !heads_ok(num_q_heads, num_kv_heads)) return 0;
-  return prompt_ws(nullptr, T, B, num_q_heads, num_kv_heads).total;
+  const size_t prompt = prompt_ws(nullptr, T, B, num_q_heads, num_kv_heads).total, rows = rows_ws(nullptr).total;
+  return prompt > rows ? prompt : rows;
 }
 
 int flint_attn_decode(const void* q, long long q_stride, const flint_kv_cache* cache, const int32_t* block_table,

@@ -778,7 +778,7 @@ bool make_map(CUtensorMap* m, const AttnArgs& a, const uint16_t* base, int box) 
 
 PromptWs prompt_ws(void* base, int T, int B, int nq, int nkv) {
   uint8_t* b = static_cast<uint8_t*>(base);
-  size_t off = 256;  // the status word
+  size_t off = kAttnData;
   auto take = [&](size_t n) {
     uint8_t* p = b + off;
     off += (n + 255) / 256 * 256;
@@ -786,7 +786,8 @@ PromptWs prompt_ws(void* base, int T, int B, int nq, int nkv) {
   };
   const size_t entries = (size_t)T * (nq / nkv) / kUnitRows + B;
   PromptWs w;
-  w.count = reinterpret_cast<int*>(take(2 * kPromptCtas * sizeof(int)));
+  static_assert(kAttnPromptCounters + 2 * kPromptCtas * sizeof(int) <= kAttnData, "counters overlap");
+  w.count = reinterpret_cast<int*>(b + kAttnPromptCounters);
   w.parts = reinterpret_cast<float*>(take((size_t)2 * kPromptCtas * kPartFloats * sizeof(float)));
   w.starts = reinterpret_cast<int4*>(take((kPromptCtas + 1) * sizeof(int4)));
   w.head = reinterpret_cast<long long*>(take(2 * sizeof(long long)));

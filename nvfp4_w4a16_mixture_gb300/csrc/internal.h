@@ -227,7 +227,20 @@ struct AttnArgs {
   float* lse;     // [T, nq] or null
   int* status;
 };
-cudaError_t launch_attn_rows(const AttnArgs& a, cudaStream_t st);
+// Workspaces of both attention kernels: the status word, each kernel's
+// counters (zero between calls) at a place of its own, then data.
+constexpr size_t kAttnRowsCounters = 256, kAttnPromptCounters = 1024, kAttnData = 4096;
+
+// Its work is cut into equal pieces, one per CTA; a unit that several CTAs
+// share is joined through the workspace.
+constexpr int kRowsCtas = 152;  // most CTAs of its grid (one per SM)
+struct RowsWs {
+  int* count;    // [kRowsCtas]: finished parts of a shared unit, zero between calls
+  float* parts;  // [2 * kRowsCtas] slots
+  size_t total;
+};
+RowsWs rows_ws(void* base);
+cudaError_t launch_attn_rows(const AttnArgs& a, const RowsWs& w, cudaStream_t st);
 
 // Prompt attention on tcgen05 (attn_prompt.cu): its plan and the partial
 // results of units that several CTAs share, in the workspace.

@@ -118,6 +118,8 @@ DECODE = [
     ([90] * 70, 4, 2, 16),
     ([8200, 17, 0, 4100], 40, 8, 256),
     ([0], 8, 2, 16),
+    ([0] * 5 + [30] * 400 + [0, 1000, 0] + [3] * 130, 4, 2, 16),  # more sequences than threads
+    ([20000], 8, 1, 16),
 ]
 
 
@@ -321,6 +323,30 @@ def test_prompt_rising_scores():
         p.k[p.table[0][i // 16], i % 16, 0] = (unit * (i * 0.25)).bfloat16()
     out, lse = run_prompt(p)
     check(out, lse, p.expect(SCALE, P_BF16), "rising")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("lens,qlens", [([300, 40], [300, 40]), ([2000, 1], [5, 1]), ([0, 10], [3, 20])])
+def test_prompt_on_a_cache_with_shared_heads(lens, qlens):
+    """One stored head read as four (a head stride of 0): no tiled copies, and
+    the same workspace afterwards serves a call that uses them."""
+    one = Problem(lens, qlens, 12, 1, 16, seed=29)
+    g = one.gpu()
+    for name in ("k_cache", "v_cache"):
+        g[name] = g[name].expand(-1, -1, 4, -1)
+    one.k, one.v = (c.expand(-1, -1, 4, -1) for c in (one.k, one.v))
+    one.nkv = 4
+    T = one.cu[-1]
+    ws = torch.zeros(fm.flint_attn_prompt_workspace_bytes(T, 2, 12, 4), dtype=torch.uint8, device="cuda")
+    lse = torch.empty(T, 12, dtype=torch.float32, device="cuda")
+    want = one.expect(SCALE, P_BF16)
+    for _ in range(2):
+        out = fm.flint_attn_prompt(**g, lse=lse, workspace=ws)
+        check(out, lse, want, "shared heads")
+        packed = {**g, "k_cache": g["k_cache"].contiguous(), "v_cache": g["v_cache"].contiguous()}
+        out = fm.flint_attn_prompt(**packed, lse=lse, workspace=ws)
+        check(out, lse, want, "copied heads")
+    assert fm.flint_moe_status(ws) == fm.FLINT_OK
 
 
 @pytest.mark.gpu
