@@ -7,7 +7,6 @@ library cannot be built or loaded this module raises: there is no fallback.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import threading
 
@@ -414,75 +413,117 @@ def flint_qkv_fused(x, residual, norm_weight, eps: float, weight, weight_scale, 
 
 
 # ------------------------------------------------ the paged cache's operators
-def _want(t, where: str, dtype, *shape, contiguous: bool = True) -> None:
-    """Refuses a tensor of another type, shape (None: any extent), place or,
-    where asked, layout: the kernels would read it as something else."""
-    ok = t.dtype == dtype and t.dim() == len(shape) and all(n is None or n == m for n, m in zip(shape, t.shape))
-    if not ok or t.device.type != "cuda" or (contiguous and not t.is_contiguous()):
-        raise FlintMoEError(FLINT_ERR_INVALID_ARG, where)
+# These calls are short beside Python's own time, so their checks read each
+# attribute once, in place: a decode call costs about 13 us of host time.
+_BF16, _F32, _I32, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
 
 
-def _on(stream):
-    """Context in which new tensors belong to `stream`."""
+def _bad(where: str):
+    return FlintMoEError(FLINT_ERR_INVALID_ARG, where)
+
+
+def _fits(t, dtype, shape, dev: int) -> bool:
+    """A contiguous tensor of this type and shape on this device."""
+    return t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous()
+
+
+def _raw_stream(stream, dev: int):
+    """The CUDA stream handle of `stream`, by default the device's current one."""
     if stream is None:
-        return contextlib.nullcontext()
-    if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(int(stream)) if int(stream) else torch.cuda.default_stream()
-    return torch.cuda.stream(stream)
+        return torch._C._cuda_getCurrentRawStream(dev)
+    return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
 
 
-def _cache(k_cache, v_cache, where: str) -> flint_kv_cache:
-    for c in (k_cache, v_cache):
-        _want(c, where, torch.bfloat16, None, None, None, 128, contiguous=False)
-    if k_cache.shape != v_cache.shape or k_cache.stride() != v_cache.stride() or k_cache.stride(3) != 1:
-        raise FlintMoEError(FLINT_ERR_INVALID_ARG, where)
-    n, bs, heads, _ = k_cache.shape
-    return flint_kv_cache(_ptr(k_cache), _ptr(v_cache), k_cache.stride(0), k_cache.stride(1), k_cache.stride(2),
-                          n, bs, heads)
+def _zeros_on(n: int, stream, dev: int):
+    """A zeroed workspace that belongs to `stream`."""
+    if stream is None:
+        return torch.zeros(n, dtype=_U8, device=dev)
+    with torch.cuda.stream(_as_stream(stream)):
+        return torch.zeros(n, dtype=_U8, device=dev)
+
+
+def _empty_on(shape, dtype, stream, dev: int):
+    """A new tensor that belongs to `stream`."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    with torch.cuda.stream(_as_stream(stream)):
+        return torch.empty(shape, dtype=dtype, device=dev)
+
+
+def _as_stream(stream):
+    if isinstance(stream, torch.cuda.Stream):
+        return stream
+    return torch.cuda.ExternalStream(int(stream)) if int(stream) else torch.cuda.default_stream()
+
+
+def _cache(k_cache, v_cache, where: str, dev: int) -> flint_kv_cache:
+    shape, strides = k_cache.shape, k_cache.stride()
+    if (len(shape) != 4 or shape[3] != 128 or strides[3] != 1 or v_cache.shape != shape or
+            v_cache.stride() != strides or k_cache.dtype is not _BF16 or v_cache.dtype is not _BF16 or
+            k_cache.get_device() != dev or v_cache.get_device() != dev):
+        raise _bad(where)
+    return flint_kv_cache(k_cache.data_ptr(), v_cache.data_ptr(), strides[0], strides[1], strides[2], shape[0],
+                          shape[1], shape[2])
+
+
+def _device(t, where: str) -> int:
+    dev = t.get_device()
+    if dev < 0:
+        raise _bad(where)
+    return dev
 
 
 def flint_attn_decode_workspace_bytes(B: int, num_q_heads: int, num_kv_heads: int) -> int:
     """Workspace bytes of flint_attn_decode (0 for an invalid shape)."""
-    return int(load().flint_attn_decode_workspace_bytes(int(B), int(num_q_heads), int(num_kv_heads)))
+    return (_lib or load()).flint_attn_decode_workspace_bytes(B, num_q_heads, num_kv_heads)
 
 
 def flint_attn_prompt_workspace_bytes(T: int, B: int, num_q_heads: int, num_kv_heads: int) -> int:
     """Workspace bytes of flint_attn_prompt (0 for an invalid shape)."""
-    return int(load().flint_attn_prompt_workspace_bytes(int(T), int(B), int(num_q_heads), int(num_kv_heads)))
+    return (_lib or load()).flint_attn_prompt_workspace_bytes(T, B, num_q_heads, num_kv_heads)
 
 
 def _attention(where, q, k_cache, v_cache, block_table, cu_q, seq_lens, scale, out, lse, workspace, stream):
-    c = _cache(k_cache, v_cache, where)
-    _want(q, where, torch.bfloat16, None, None, contiguous=False)
+    lib = _lib or load()
+    dev = _device(q, where)
+    c = _cache(k_cache, v_cache, where, dev)
+    if q.dim() != 2 or seq_lens.dim() != 1 or block_table.dim() != 2:
+        raise _bad(where)
     T, width = q.shape
-    nq, B = width // 128, seq_lens.shape[0] if seq_lens.dim() == 1 else -1
-    _want(seq_lens, where, torch.int32, None if cu_q is not None else T)
-    _want(block_table, where, torch.int32, B, None, contiguous=False)
-    if cu_q is not None:
-        _want(cu_q, where, torch.int32, B + 1)
-    if width != nq * 128 or q.stride(1) != 1 or (block_table.shape[1] > 1 and block_table.stride(1) != 1):
-        raise FlintMoEError(FLINT_ERR_INVALID_ARG, where)
-    for t, dtype, n in ((out, torch.bfloat16, width), (lse, torch.float32, nq)):
-        if t is not None:
-            _want(t, where, dtype, T, n)
-    if workspace is not None:
-        _want(workspace, where, torch.uint8, None)
-    with _on(stream):
-        if out is None:
-            out = torch.empty(T, width, dtype=torch.bfloat16, device=q.device)
-        if workspace is None:
-            need = (flint_attn_decode_workspace_bytes(B, nq, c.num_kv_heads) if cu_q is None else
-                    flint_attn_prompt_workspace_bytes(T, B, nq, c.num_kv_heads))
-            workspace = torch.zeros(max(1, need), dtype=torch.uint8, device=q.device)
-    table_stride = block_table.stride(0) if B > 1 else block_table.shape[1]
-    q_stride = q.stride(0) if T > 1 else width
-    scale = float(scale) if scale is not None else 128 ** -0.5
-    common = (_ptr(q), q_stride, ctypes.byref(c), _ptr(block_table), table_stride, block_table.shape[1])
-    rest = (B, nq, scale, _ptr(out), _ptr(lse), _ptr(workspace), workspace.numel(), _stream(stream))
+    B, cols = block_table.shape
+    q_stride, q_unit = q.stride()
+    t_stride, t_unit = block_table.stride()
+    nq = width // 128
+    if (q.dtype is not _BF16 or q_unit != 1 or width != nq * 128 or block_table.dtype is not _I32 or
+            block_table.get_device() != dev or (t_unit != 1 and cols > 1) or
+            not _fits(seq_lens, _I32, (B,), dev) or (T != B if cu_q is None else not _fits(cu_q, _I32, (B + 1,), dev)) or
+            (out is not None and not _fits(out, _BF16, (T, width), dev)) or
+            (lse is not None and not _fits(lse, _F32, (T, nq), dev))):
+        raise _bad(where)
+    if out is None:
+        out = _empty_on((T, width), _BF16, stream, dev)
+    if workspace is None:
+        need = (lib.flint_attn_decode_workspace_bytes(B, nq, c.num_kv_heads) if cu_q is None else
+                lib.flint_attn_prompt_workspace_bytes(T, B, nq, c.num_kv_heads))
+        workspace = _zeros_on(max(1, need), stream, dev)
+    elif workspace.get_device() != dev or not workspace.is_contiguous():
+        raise _bad(where)
+    ws, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    if scale is None:
+        scale = 128 ** -0.5
+    if T <= 1:
+        q_stride = width
+    if B <= 1:
+        t_stride = cols
+    lse = None if lse is None else lse.data_ptr()
+    st = _raw_stream(stream, dev)
     if cu_q is None:
-        rc = load().flint_attn_decode(*common, _ptr(seq_lens), *rest)
+        rc = lib.flint_attn_decode(q.data_ptr(), q_stride, c, block_table.data_ptr(), t_stride, cols,
+                                   seq_lens.data_ptr(), B, nq, scale, out.data_ptr(), lse, ws, ws_bytes, st)
     else:
-        rc = load().flint_attn_prompt(*common, _ptr(cu_q), _ptr(seq_lens), T, *rest)
+        rc = lib.flint_attn_prompt(q.data_ptr(), q_stride, c, block_table.data_ptr(), t_stride, cols,
+                                   cu_q.data_ptr(), seq_lens.data_ptr(), T, B, nq, scale, out.data_ptr(), lse, ws,
+                                   ws_bytes, st)
     if rc != FLINT_OK:
         raise FlintMoEError(rc, where)
     return out
@@ -515,7 +556,7 @@ def flint_attn_prompt(q, k_cache, v_cache, block_table, cu_q, seq_lens, scale=No
 def flint_kv_workspace_bytes(num_blocks: int) -> int:
     """Workspace bytes of flint_kv_copy_pages and flint_kv_compact_plan (0 for
     an invalid pool)."""
-    return int(load().flint_kv_workspace_bytes(int(num_blocks)))
+    return (_lib or load()).flint_kv_workspace_bytes(num_blocks)
 
 
 def flint_kv_copy_pages(k_cache, v_cache, moves, tokens=None, count=None, workspace=None, stream=None) -> None:
@@ -523,18 +564,20 @@ def flint_kv_copy_pages(k_cache, v_cache, moves, tokens=None, count=None, worksp
     [n, 2]); of tokens[i] slots only when tokens (int32 [n]) is given, and of
     the first count[0] pairs only when count (int32 [1], on the device) is."""
     where = "flint_kv_copy_pages"
-    c = _cache(k_cache, v_cache, where)
-    _want(moves, where, torch.int32, None, 2)
-    if tokens is not None:
-        _want(tokens, where, torch.int32, moves.shape[0])
-    if count is not None:
-        _want(count, where, torch.int32, 1)
-    with _on(stream):
-        if workspace is None:
-            workspace = torch.zeros(max(1, flint_kv_workspace_bytes(c.num_blocks)), dtype=torch.uint8,
-                                    device=k_cache.device)
-    rc = load().flint_kv_copy_pages(ctypes.byref(c), _ptr(moves), moves.shape[0], _ptr(count), _ptr(tokens),
-                                    _ptr(workspace), workspace.numel(), _stream(stream))
+    lib = _lib or load()
+    dev = _device(k_cache, where)
+    c = _cache(k_cache, v_cache, where, dev)
+    n = moves.shape[0] if moves.dim() == 2 else -1
+    if (not _fits(moves, _I32, (n, 2), dev) or (tokens is not None and not _fits(tokens, _I32, (n,), dev)) or
+            (count is not None and not _fits(count, _I32, (1,), dev))):
+        raise _bad(where)
+    if workspace is None:
+        workspace = _zeros_on(max(1, lib.flint_kv_workspace_bytes(c.num_blocks)), stream, dev)
+    elif workspace.get_device() != dev or not workspace.is_contiguous():
+        raise _bad(where)
+    rc = lib.flint_kv_copy_pages(c, moves.data_ptr(), n, None if count is None else count.data_ptr(),
+                                 None if tokens is None else tokens.data_ptr(), workspace.data_ptr(),
+                                 workspace.numel() * workspace.element_size(), _raw_stream(stream, dev))
     if rc != FLINT_OK:
         raise FlintMoEError(rc, where)
 
@@ -546,29 +589,33 @@ def flint_kv_compact_plan(block_table, seq_lens, block_size: int, num_blocks: in
     pages in use, pairs).  flint_kv_copy_pages(k_cache, v_cache, moves,
     count=counts[1:]) then moves the pages."""
     where = "flint_kv_compact_plan"
-    _want(seq_lens, where, torch.int32, None)
-    B = seq_lens.shape[0]
-    _want(block_table, where, torch.int32, B, None, contiguous=False)
-    width, pairs = block_table.shape[1], max(0, int(num_blocks)) // 2
-    if width > 1 and block_table.stride(1) != 1:
-        raise FlintMoEError(FLINT_ERR_INVALID_ARG, where)
-    for t, shape in ((new_table, (B, width)), (moves, (pairs, 2)), (counts, (2,))):
-        if t is not None:
-            _want(t, where, torch.int32, *shape)
-    dev = seq_lens.device
-    with _on(stream):
-        if new_table is None:
-            new_table = torch.empty(B, width, dtype=torch.int32, device=dev)
-        if moves is None:
-            moves = torch.empty(pairs, 2, dtype=torch.int32, device=dev)
-        if counts is None:
-            counts = torch.empty(2, dtype=torch.int32, device=dev)
-        if workspace is None:
-            workspace = torch.zeros(max(1, flint_kv_workspace_bytes(num_blocks)), dtype=torch.uint8, device=dev)
-    rc = load().flint_kv_compact_plan(_ptr(block_table), block_table.stride(0) if B > 1 else width, width,
-                                      _ptr(seq_lens), B, int(block_size), int(num_blocks), _ptr(new_table),
-                                      _ptr(moves), _ptr(counts), _ptr(workspace), workspace.numel(),
-                                      _stream(stream))
+    lib = _lib or load()
+    dev = _device(seq_lens, where)
+    if block_table.dim() != 2:
+        raise _bad(where)
+    B, cols = block_table.shape
+    t_stride, t_unit = block_table.stride()
+    pairs = max(0, num_blocks) // 2
+    if (block_table.dtype is not _I32 or block_table.get_device() != dev or (t_unit != 1 and cols > 1) or
+            not _fits(seq_lens, _I32, (B,), dev) or
+            (new_table is not None and not _fits(new_table, _I32, (B, cols), dev)) or
+            (moves is not None and not _fits(moves, _I32, (pairs, 2), dev)) or
+            (counts is not None and not _fits(counts, _I32, (2,), dev))):
+        raise _bad(where)
+    if new_table is None:
+        new_table = _empty_on((B, cols), _I32, stream, dev)
+    if moves is None:
+        moves = _empty_on((pairs, 2), _I32, stream, dev)
+    if counts is None:
+        counts = _empty_on((2,), _I32, stream, dev)
+    if workspace is None:
+        workspace = _zeros_on(max(1, lib.flint_kv_workspace_bytes(num_blocks)), stream, dev)
+    elif workspace.get_device() != dev or not workspace.is_contiguous():
+        raise _bad(where)
+    rc = lib.flint_kv_compact_plan(block_table.data_ptr(), t_stride if B > 1 else cols, cols, seq_lens.data_ptr(), B,
+                                   block_size, num_blocks, new_table.data_ptr(), moves.data_ptr(),
+                                   counts.data_ptr(), workspace.data_ptr(),
+                                   workspace.numel() * workspace.element_size(), _raw_stream(stream, dev))
     if rc != FLINT_OK:
         raise FlintMoEError(rc, where)
     return new_table, moves, counts

@@ -139,6 +139,17 @@ cudaError_t device_sms(int* sms) {
   return cudaSuccess;
 }
 
+cudaError_t allow_smem(const void* fn, int bytes, std::atomic<bool> (&done)[64]) {
+  int dev = 0;
+  cudaError_t err = cudaGetDevice(&dev);
+  if (err != cudaSuccess) return err;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (done[dev].load(std::memory_order_relaxed)) return cudaSuccess;
+  err = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (err == cudaSuccess) done[dev].store(true, std::memory_order_relaxed);
+  return err;
+}
+
 }  // namespace flint
 
 using namespace flint;

@@ -76,9 +76,9 @@ int attention(bool prompt, const void* q, long long q_stride, const flint_kv_cac
   a.lse = lse;
   a.status = static_cast<int*>(workspace);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  const cudaError_t err = prompt && attn_prompt_supported(a)
-                              ? launch_attn_prompt(a, prompt_ws(workspace, T, B, nq, a.nkv), st)
-                              : launch_attn_rows(a, rows_ws(workspace), st);
+  cudaError_t err = cudaErrorNotSupported;
+  if (prompt) err = launch_attn_prompt(a, prompt_ws(workspace, T, B, nq, a.nkv), st);
+  if (err == cudaErrorNotSupported) err = launch_attn_rows(a, rows_ws(workspace), st);
   return err == cudaSuccess ? FLINT_OK : FLINT_ERR_CUDA;
 }
 

@@ -798,11 +798,6 @@ PromptWs prompt_ws(void* base, int T, int B, int nq, int nkv) {
   return w;
 }
 
-bool attn_prompt_supported(const AttnArgs& a) {
-  CUtensorMap m;
-  return make_map(&m, a, a.k, box_rows(a.block_size));
-}
-
 cudaError_t launch_attn_prompt(const AttnArgs& a, const PromptWs& w, cudaStream_t st) {
   Args p;
   p.a = a;
@@ -810,18 +805,22 @@ cudaError_t launch_attn_prompt(const AttnArgs& a, const PromptWs& w, cudaStream_
   p.box = box_rows(a.block_size);
   for (p.box_log2 = 0; (1 << p.box_log2) < p.box;) ++p.box_log2;
   Maps maps;
-  if (!make_map(&maps.k, a, a.k, p.box) || !make_map(&maps.v, a, a.v, p.box)) return cudaErrorInvalidValue;
+  if (!make_map(&maps.k, a, a.k, p.box) || !make_map(&maps.v, a, a.v, p.box)) return cudaErrorNotSupported;
   int sms = 0;
   cudaError_t err = device_sms(&sms);
   if (err != cudaSuccess) return err;
   int ctas = sms < kPromptCtas ? sms : kPromptCtas;
   const void* fn = reinterpret_cast<const void*>(attn_prompt_kernel);
-  err = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+  static std::atomic<bool> allowed[64], checked;
+  err = allow_smem(fn, (int)kSmem, allowed);
   if (err != cudaSuccess) return err;
-  cudaFuncAttributes fa;
-  err = cudaFuncGetAttributes(&fa, fn);
-  if (err != cudaSuccess) return err;
-  if (fa.numRegs != kRegsLaunch) return cudaErrorInvalidConfiguration;  // the register split needs them
+  if (!checked.load(std::memory_order_relaxed)) {
+    cudaFuncAttributes fa;
+    err = cudaFuncGetAttributes(&fa, fn);
+    if (err != cudaSuccess) return err;
+    if (fa.numRegs != kRegsLaunch) return cudaErrorInvalidConfiguration;  // the register split needs them
+    checked.store(true, std::memory_order_relaxed);
+  }
   cudaLaunchConfig_t cfg = {};
   cfg.stream = st;
   cudaLaunchAttribute attr[1];

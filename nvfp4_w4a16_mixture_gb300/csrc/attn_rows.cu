@@ -551,7 +551,8 @@ __global__ void __launch_bounds__(kRowsThreads, 1) attn_rows_kernel(const __grid
 template <int NT>
 cudaError_t launch_nt(const AttnArgs& a, const RowsWs& w, cudaStream_t st) {
   const void* fn = reinterpret_cast<const void*>(attn_rows_kernel<NT>);
-  cudaError_t err = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem<NT>);
+  static std::atomic<bool> allowed[64];
+  cudaError_t err = allow_smem(fn, (int)kSmem<NT>, allowed);
   if (err != cudaSuccess) return err;
   int sms = 0;
   err = device_sms(&sms);

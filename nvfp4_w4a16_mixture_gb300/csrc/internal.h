@@ -1,6 +1,8 @@
 // Internal interface between the C-ABI entry points and the kernels.
 #pragma once
 
+#include <atomic>
+
 #include <cuda_runtime.h>
 #include <stddef.h>
 #include <stdint.h>
@@ -207,6 +209,10 @@ cudaError_t launch_bf16_experts(const MoEArgs& a, const uint16_t* w13, const uin
 // Streaming multiprocessors of the current device (cached per device).
 cudaError_t device_sms(int* sms);
 
+// Lets kernel `fn` use `bytes` of dynamic shared memory on the current device;
+// `done` (one flag per device, the caller's own) is set once that holds.
+cudaError_t allow_smem(const void* fn, int bytes, std::atomic<bool> (&done)[64]);
+
 // Attention over the paged cache (attn_rows.cu).  Decode: cu_q is null, T = B
 // and sequence b owns row b.
 struct AttnArgs {
@@ -256,7 +262,8 @@ struct PromptWs {
   size_t total;
 };
 PromptWs prompt_ws(void* base, int T, int B, int nq, int nkv);
-bool attn_prompt_supported(const AttnArgs& a);
+// cudaErrorNotSupported, with nothing enqueued, for a cache whose strides no
+// tensor map takes.
 cudaError_t launch_attn_prompt(const AttnArgs& a, const PromptWs& w, cudaStream_t st);
 cudaError_t span_buffer_set_attn_prompt(unsigned long long* b);
 
