@@ -76,9 +76,8 @@ int attention(bool prompt, const void* q, long long q_stride, const flint_kv_cac
   a.lse = lse;
   a.status = static_cast<int*>(workspace);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  cudaError_t err = cudaErrorNotSupported;
-  if (prompt) err = launch_attn_prompt(a, prompt_ws(workspace, T, B, nq, a.nkv), st);
-  if (err == cudaErrorNotSupported) err = launch_attn_rows(a, rows_ws(workspace), st);
+  const cudaError_t err = prompt ? launch_attn_prompt(a, prompt_ws(workspace, T, B, nq, a.nkv), st)
+                                 : launch_attn_rows(a, rows_ws(workspace), st);
   return err == cudaSuccess ? FLINT_OK : FLINT_ERR_CUDA;
 }
 
@@ -93,8 +92,7 @@ size_t flint_attn_decode_workspace_bytes(int B, int num_q_heads, int num_kv_head
 
 size_t flint_attn_prompt_workspace_bytes(int T, int B, int num_q_heads, int num_kv_heads) {
   if (T < 0 || B < 0 || !heads_ok(num_q_heads, num_kv_heads)) return 0;
-  const size_t prompt = prompt_ws(nullptr, T, B, num_q_heads, num_kv_heads).total, rows = rows_ws(nullptr).total;
-  return prompt > rows ? prompt : rows;
+  return prompt_ws(nullptr, T, B, num_q_heads, num_kv_heads).total;
 }
 
 int flint_attn_decode(const void* q, long long q_stride, const flint_kv_cache* cache, const int32_t* block_table,

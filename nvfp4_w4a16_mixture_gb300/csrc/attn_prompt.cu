@@ -15,16 +15,21 @@
 // it moves (and O and the sum are rescaled) only when some score exceeds it
 // by more than 8, so P stays below 2^8 and O is seldom touched.
 //
-// One CTA per SM, 12 warps (two idle, there to make up the third warpgroup
-// whose registers the softmax takes over):
+// One CTA per SM, 12 warps, the third warpgroup leaving registers to the
+// softmax:
 //   warps 0-3, 4-7: softmax of row tile 0, 1 (thread = row): Q into swizzled
 //     shared memory, then per key tile S from TMEM, P back, and at the
 //     unit's end O to the output;
 //   warp 8: MMA issue.  Order S_0(0) S_1(0), then per j: PV_0(j) S_0(j+1)
 //     PV_1(j) S_1(j+1): while one tile's softmax runs, the other's products
 //     do;
-//   warp 9: TMA of the key and value tiles (a ring of five 32 KB stages), as
-//     boxes of gcd(page, 128) rows, the pages looked up one per lane.
+//   warps 9, 11: the key and the value tiles (a ring of five 32 KB stages, K_0
+//     V_0 K_1 V_1 ..) by 16-byte asynchronous copies, the pages looked up one
+//     key per lane.  Tiled bulk copies would need a box per page: at 16 slots a
+//     page 32 boxes for a pair of tiles, about 90 cycles each, 4,500 cycles in
+//     all where the products take 2,048; and page sizes and strides that no
+//     tensor map takes would need another path;
+//   warp 10: walks along the CTA's work and publishes it to the others.
 // Shared memory: Q 2 x 32 KB, ring 5 x 32 KB.  TMEM: S_0, S_1, O_0, O_1, 128
 // columns each.
 //
@@ -35,12 +40,9 @@
 // the parts in CTA order, so the result does not depend on which one that is.
 //
 // Keys past a sequence's end or on a page outside the cache: their scores
-// become -inf and their V rows are zeroed in shared memory before the product
-// (whatever the slots hold).  Every wait is bounded (FLINT_ERR_TIMEOUT in the
+// become -inf, and their rows in shared memory are zeros (whatever the slots
+// hold).  Every wait is bounded (FLINT_ERR_TIMEOUT in the
 // status word on expiry).
-#include <cuda.h>
-#include <cudaTypedefs.h>
-
 #include "attn.cuh"
 #include "tc.cuh"
 
@@ -54,13 +56,15 @@ constexpr int kStageBytes = 2 * kHalf;
 constexpr int kStages = 5;
 constexpr int kOffRing = 2 * kStageBytes;  // after Q_0, Q_1
 constexpr int kOffCtl = kOffRing + kStages * kStageBytes;
-constexpr int kWarpMma = 8, kWarpLoad = 9;
-constexpr int kThreads = 384;              // three warpgroups
-// Registers per thread: 168 at launch (65536 / 384, in eights); the two
-// softmax warpgroups take what the third gives up: 2 * 216 + 72 = 3 * 168.
-constexpr int kRegsLaunch = 168, kRegsSoftmax = 216, kRegsOther = 72;
-static_assert(2 * kRegsSoftmax + kRegsOther <= 3 * kRegsLaunch, "setmaxnreg.inc would wait for ever");
+constexpr int kWarpMma = 8, kWarpWalk = 9, kWarpLoad = 12;  // 12 .. 15: K, V, K, V
+constexpr int kThreads = 512;              // four warpgroups
+// Registers per thread: 128 at launch (65536 / 512); the two softmax
+// warpgroups take what the others give up: 2 * 200 + 2 * 56 = 4 * 128.
+constexpr int kRegsLaunch = 128, kRegsSoftmax = 200, kRegsOther = 56;
+static_assert(2 * kRegsSoftmax + 2 * kRegsOther <= 4 * kRegsLaunch, "setmaxnreg.inc would wait for ever");
 constexpr int kInfo = 8;                   // key-tile records in flight
+constexpr int kPieces = 4;                 // pieces published ahead
+constexpr int kPieceReaders = 13;          // the softmax warps, the MMA and the load warps
 constexpr int kUnitWeight = 3;             // a unit's fixed part, in tile products
 constexpr int kMinWeight = 8;              // least work of a CTA
 constexpr float kLazy = 8.0f;
@@ -70,15 +74,26 @@ constexpr int kPartFloats = kUnitRows * (kHeadDim + 2);
 
 struct TileInfo {
   int keys;         // valid keys of the tile (from its start)
-  uint32_t bad[4];  // boxes on a page outside the cache
+  int some_bad[2];  // whether there is a bit in its first or second two words
+  uint32_t bad[4];  // keys on a page outside the cache
+};
+// One part of a unit: the CTA's next work, published by the walking warp.
+struct Piece {
+  int b, lo, n, keys;   // sequence, its first q row, its q rows, its keys
+  int r0, rows, h;      // packed rows, kv head
+  int t0, t1;           // key tiles
+  int c_first, c_last;  // CTAs that share the unit
+  int valid;            // 0: the end
 };
 struct Ctl {
   uint64_t full[kStages], empty[kStages];
-  uint64_t q_full[2], s_full[2], p_full[2], o_full[2], o_free[2], wg[2];
+  uint64_t q_full[2], s_full[2], p_full[2][2], o_full[2], o_free[2], wg[2];
+  uint64_t piece_full[kPieces], piece_empty[kPieces];
   uint32_t tmem;
   int abort;
   int last[2];
   TileInfo info[kInfo];
+  Piece piece[kPieces];
 };
 constexpr size_t kSmem = (size_t)kOffCtl + sizeof(Ctl) + 1024;
 
@@ -106,13 +121,12 @@ FLINT_DEV bool wait(uint64_t* bar, uint32_t parity, volatile int* abort, int* st
 struct Args {
   AttnArgs a;
   PromptWs w;
-  int box, box_log2;  // rows of a TMA box: gcd(block_size, 128)
-};
-struct Maps {
-  CUtensorMap k, v;  // {128, heads, slots, pages}, box {64, 1, box, 1}
 };
 
 // ---------------------------------------------------------------- the plan
+// A CTA's start record: {entry, kv head, offset in the unit, CTAs at work},
+// {total weight, the piece's weight} as 64-bit values, the entry.
+constexpr int kStartWords = 4;
 // Entry: up to 256 packed rows of a sequence (all kv heads).
 struct Entry {
   int b, lo, n, keys;     // sequence, its first q row, its q rows, its keys
@@ -120,8 +134,8 @@ struct Entry {
 };
 FLINT_DEV long long weight(const Entry& e) { return (long long)e.tiles * e.mul + kUnitWeight; }
 
-FLINT_DEV Entry load_entry(const PromptWs& w, int i) {
-  const uint4 x = ldg_cg_v4(w.entries + 2 * (long long)i), y = ldg_cg_v4(w.entries + 2 * (long long)i + 1);
+FLINT_DEV Entry load_entry(const int4* p) {
+  const uint4 x = ldg_cg_v4(p), y = ldg_cg_v4(p + 1);
   Entry e;
   e.b = (int)x.x; e.lo = (int)x.y; e.n = (int)x.z; e.keys = (int)x.w;
   e.r0 = (int)y.x; e.rows = (int)y.y; e.tiles = (int)y.z; e.mul = (int)y.w;
@@ -202,91 +216,96 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const Args p, i
   for (long long e0 = 0; e0 < n_entries; e0 += kPlanThreads) {
     const long long e = e0 + tid;
     long long all;
-    const long long at = total + scan_cta64(e < n_entries ? weight(load_entry(p.w, (int)e)) * a.nkv : 0, warps, &all);
+    const long long at = total + scan_cta64(e < n_entries ? weight(load_entry(p.w.entries + 2 * e)) * a.nkv : 0, warps, &all);
     if (e < n_entries) p.w.prefix[e] = at;
     total += all;
   }
   if (tid == 0) p.w.prefix[n_entries] = total;
   __syncthreads();
   const long long n_cta = total == 0 ? 0 : max(1ll, min((long long)ctas, total / kMinWeight));
-  if (tid == 0) {
-    p.w.head[0] = total;
-    p.w.head[1] = n_cta;
-  }
+  if (tid < ctas && tid >= n_cta) p.w.starts[kStartWords * tid] = make_int4(0, 0, 0, 0);
   // CTA c's piece begins at floor(c total / n_cta); entry e writes those inside it
   for (long long e = tid; e < n_entries; e += kPlanThreads) {
-    const Entry x = load_entry(p.w, (int)e);
-    const long long w = weight(x), at = p.w.prefix[e], end = at + w * a.nkv;
+    const long long w = weight(load_entry(p.w.entries + 2 * e)), at = p.w.prefix[e], end = at + w * a.nkv;
     for (long long c = (at * n_cta + total - 1) / total; c < n_cta; ++c) {
       const long long pos = c * total / n_cta;
       if (pos >= end) break;
-      if (pos < at) continue;
-      p.w.starts[c] = make_int4((int)e, (int)((pos - at) / w), (int)((pos - at) % w), 0);
+      const long long rem = (c + 1) * total / n_cta - pos;
+      int4* s = p.w.starts + kStartWords * c;
+      s[0] = make_int4((int)e, (int)((pos - at) / w), (int)((pos - at) % w), (int)n_cta);
+      s[1] = make_int4((int)total, (int)(total >> 32), (int)rem, (int)(rem >> 32));
+      s[2] = p.w.entries[2 * e];
+      s[3] = p.w.entries[2 * e + 1];
     }
   }
 }
 
 // ------------------------------------------------------------- the pieces
-// One CTA's walk along its piece: the same in every role.
-struct Walk {
-  const PromptWs* w;
-  int nkv;
-  long long total, ctas, rem;
-  int cta, i, h, off;
-  Entry e;
-  // the current step
-  int t0, t1;          // key tiles
-  int c_first, c_last; // CTAs that share the unit
-};
-
-FLINT_DEV bool walk_start(Walk& k, const Args& p) {
-  k.w = &p.w;
-  k.nkv = p.a.nkv;
-  k.cta = blockIdx.x;
-  const uint4 hd = ldg_cg_v4(p.w.head);
-  k.total = (long long)hd.x | ((long long)hd.y << 32);
-  k.ctas = (long long)hd.z | ((long long)hd.w << 32);
-  if (k.cta >= k.ctas) return false;
-  const long long at = k.cta * k.total / k.ctas;
-  k.rem = (k.cta + 1) * k.total / k.ctas - at;
-  const uint4 s = ldg_cg_v4(p.w.starts + k.cta);
-  k.i = (int)s.x; k.h = (int)s.y; k.off = (int)s.z;
-  k.e = load_entry(p.w, k.i);
-  return true;
+// One warp walks along the CTA's piece of the line and publishes the parts of
+// units on it, a few ahead of their use.
+FLINT_DEV void walk_role(const Args& p, Ctl& C) {
+  const int lane = threadIdx.x & 31, cta = blockIdx.x, nkv = p.a.nkv;
+  volatile int* abort = &C.abort;
+  const int4* start = p.w.starts + kStartWords * cta;
+  const uint4 s0 = ldg_cg_v4(start), s1 = ldg_cg_v4(start + 1);
+  Entry e = load_entry(start + 2);
+  int i = (int)s0.x, h = (int)s0.y, off = (int)s0.z;
+  const long long ctas = (int)s0.w, total = (long long)((unsigned long long)s1.y << 32 | s1.x);
+  long long rem = ctas == 0 ? 0 : (long long)((unsigned long long)s1.w << 32 | s1.z);
+  uint32_t n = 0;
+  auto publish = [&](const Piece& x) {
+    if (n >= (uint32_t)kPieces && !wait(&C.piece_empty[n % kPieces], ((n / kPieces) - 1) & 1, abort, p.a.status))
+      return false;
+    if (lane == 0) {
+      C.piece[n % kPieces] = x;
+      mbar_arrive(&C.piece_full[n % kPieces]);
+    }
+    __syncwarp();
+    ++n;
+    return true;
+  };
+  Piece x;
+  while (rem > 0) {
+    const int w = (int)weight(e);
+    const int take = (int)min((long long)(w - off), rem);
+    const int real = max(1, e.tiles * e.mul);
+    if (off < real) {
+      x.b = e.b; x.lo = e.lo; x.n = e.n; x.keys = e.keys;
+      x.r0 = e.r0; x.rows = e.rows; x.h = h;
+      x.t0 = min(off / e.mul, e.tiles);
+      x.t1 = min((off + take) / e.mul, e.tiles);
+      x.c_first = x.c_last = cta;
+      x.valid = 1;
+      if (off > 0 || take < real) {  // CTA of position y: floor(((y + 1) ctas - 1) / total)
+        const long long at = __ldcg(p.w.prefix + i) + (long long)h * w;
+        x.c_first = (int)(((at + 1) * ctas - 1) / total);
+        x.c_last = (int)(((at + real) * ctas - 1) / total);
+      }
+      if (!publish(x)) return;
+    }
+    rem -= take;
+    off += take;
+    if (off == w) {
+      off = 0;
+      if (++h == nkv) {
+        h = 0;
+        ++i;
+        if (rem > 0) e = load_entry(p.w.entries + 2 * (long long)i);
+      }
+    }
+  }
+  x.valid = 0;
+  publish(x);
 }
 
-// The next part of a unit in this CTA's piece; false at its end.
-FLINT_DEV bool walk_next(Walk& k, Entry& u, int& h) {
-  while (k.rem > 0) {
-    const int wgt = (int)weight(k.e);
-    const int take = (int)min((long long)(wgt - k.off), k.rem);
-    const int real = max(1, k.e.tiles * k.e.mul);
-    const bool at_work = k.off < real;
-    if (at_work) {
-      u = k.e;
-      h = k.h;
-      k.t0 = min(k.off / k.e.mul, k.e.tiles);
-      k.t1 = min((k.off + take) / k.e.mul, k.e.tiles);
-      k.c_first = k.c_last = k.cta;
-      if (k.off > 0 || take < real) {  // CTA of position x: floor(((x + 1) ctas - 1) / total)
-        const long long at = __ldcg(k.w->prefix + k.i) + (long long)k.h * wgt;
-        k.c_first = (int)(((at + 1) * k.ctas - 1) / k.total);
-        k.c_last = (int)(((at + real) * k.ctas - 1) / k.total);
-      }
-    }
-    k.rem -= take;
-    k.off += take;
-    if (k.off == wgt) {
-      k.off = 0;
-      if (++k.h == k.nkv) {
-        k.h = 0;
-        ++k.i;
-        if (k.rem > 0) k.e = load_entry(*k.w, k.i);
-      }
-    }
-    if (at_work) return true;
-  }
-  return false;
+// Piece n, once it is published; false at the end (or on expiry).
+FLINT_DEV bool piece_ready(Ctl& C, uint32_t n, int* status) {
+  return wait(&C.piece_full[n % kPieces], (n / kPieces) & 1, &C.abort, status) && C.piece[n % kPieces].valid;
+}
+// This warp has read all it needs of piece n.
+FLINT_DEV void piece_done(Ctl& C, uint32_t n) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(&C.piece_empty[n % kPieces]);
 }
 
 FLINT_DEV uint32_t pack2(float a, float b) {
@@ -304,128 +323,209 @@ FLINT_DEV void store_cols(uint16_t* dst, const float* o, float inv) {
 }
 
 // -------------------------------------------------------------- the softmax
+// Two fp32 in a register pair: the packed operations are two IEEE ones.
+FLINT_DEV unsigned long long pair(float a, float b) {
+  unsigned long long r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+FLINT_DEV void unpair(unsigned long long v, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
+FLINT_DEV unsigned long long fma2(unsigned long long a, unsigned long long b, unsigned long long c) {
+  unsigned long long r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+FLINT_DEV unsigned long long add2(unsigned long long a, unsigned long long b) {
+  unsigned long long r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+FLINT_DEV float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
+FLINT_DEV float finish_lse(float m, float l) {
+  return l == 0.0f ? neg_inf() : (m + log2f(l)) * 0.6931471805599453f;
+}
+
+// Q rows of the piece's row tile t into swizzled shared memory, 16 lanes per
+// row.
+FLINT_DEV void load_q(const AttnArgs& a, const Piece& u, int t, uint8_t* sq, int warp, int lane) {
+  const int G = a.nq / a.nkv, ch = lane & 15;
+#pragma unroll
+  for (int i0 = 0; i0 < 16; i0 += 8) {
+    uint4 v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int r = 32 * warp + 2 * (i0 + i) + (lane >> 4), R = kTile * t + r;
+      const int q = u.r0 + R, token = q / G, head = u.h * G + q - token * G;
+      v[i] = R < u.rows ? ldg_cg_v4(a.q + (long long)(u.lo + token) * a.q_stride + (long long)head * kHeadDim + 8 * ch)
+                        : make_uint4(0, 0, 0, 0);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int r = 32 * warp + 2 * (i0 + i) + (lane >> 4);
+      *reinterpret_cast<uint4*>(sq + (ch >> 3) * kHalf + r * 128 + (((ch & 7) ^ (r & 7)) << 4)) = v[i];
+    }
+  }
+}
+
+// Row (of the output, in heads) of packed row R of the piece.
+FLINT_DEV long long out_row(const AttnArgs& a, const Piece& u, int R) {
+  const int G = a.nq / a.nkv, q = u.r0 + R, token = q / G;
+  return (long long)(u.lo + token) * a.nq + u.h * G + q - token * G;
+}
+
+FLINT_DEV float* part_of(const Args& p, const Piece& u, int cta) {
+  return p.w.parts + (size_t)(2 * cta + (cta == u.c_first)) * kPartFloats;
+}
+
+// The parts of a shared unit, joined in CTA order, for packed row R.
+FLINT_DEV void join_row(const Args& p, const Piece& u, int R) {
+  float m = neg_inf();
+  for (int x = u.c_first; x <= u.c_last; ++x) m = fmaxf(m, __ldcg(part_of(p, u, x) + kHeadDim * kUnitRows + R));
+  float l = 0.0f;
+  float o[4][32];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int x = 0; x < 32; ++x) o[i][x] = 0.0f;
+  for (int x = u.c_first; x <= u.c_last; ++x) {
+    const float* pp = part_of(p, u, x);
+    const float pm = __ldcg(pp + kHeadDim * kUnitRows + R), pl = __ldcg(pp + (kHeadDim + 1) * kUnitRows + R);
+    const float f = pm == neg_inf() ? (pl == 0.0f ? 0.0f : 1.0f) : ex2(pm - m);
+    l += f * pl;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+      const float4 v = __ldcg(reinterpret_cast<const float4*>(pp) + (size_t)i * kUnitRows + R);
+      o[i >> 3][4 * (i & 7)] += f * v.x;
+      o[i >> 3][4 * (i & 7) + 1] += f * v.y;
+      o[i >> 3][4 * (i & 7) + 2] += f * v.z;
+      o[i >> 3][4 * (i & 7) + 3] += f * v.w;
+    }
+  }
+  if (R < u.rows) {
+    const long long row = out_row(p.a, u, R);
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) store_cols(p.a.out + row * kHeadDim + 32 * i, o[i], inv);
+    if (p.a.lse) p.a.lse[row] = finish_lse(m, l);
+  }
+}
+
 FLINT_DEV void softmax_role(const Args& p, Ctl& C, uint8_t* smem, uint32_t tmem, int t) {
   const AttnArgs& a = p.a;
-  const int G = a.nq / a.nkv;
   const int warp = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31;
-  const int row = 32 * warp + lane;  // of the tile
+  const int R = kTile * t + 32 * warp + lane;  // packed row of the unit
   const uint32_t lanes = (uint32_t)(32 * warp) << 16;
   const uint32_t tS = tmem + lanes + (uint32_t)(kTile * t);
   const uint32_t tO = tmem + lanes + (uint32_t)(2 * kTile + kTile * t);
-  uint8_t* sq = smem + t * kStageBytes;
   const float c = a.scale * 1.4426950408889634f;
   volatile int* abort = &C.abort;
   uint32_t n_s = 0, n_o = 0, n_wg = 0;  // phases done: s_full, o_full, wg
   int n_tile = 0;                       // key tiles of the CTA so far
-  Walk k;
-  Entry u;
-  int h;
-  if (!walk_start(k, p)) return;
-  while (!*abort && walk_next(k, u, h)) {
-    const int nt = k.t1 - k.t0;
+  for (uint32_t n = 0; piece_ready(C, n, a.status); ++n) {
+    const Piece& u = C.piece[n % kPieces];
+    const int nt = u.t1 - u.t0;
     if (u.rows <= kTile * t) {  // the unit has one row tile
       n_tile += nt;
+      piece_done(C, n);
       continue;
     }
     if (nt > 0) {
-      // Q_t: 16 lanes per row
-      const int ch = lane & 15;
-#pragma unroll
-      for (int i0 = 0; i0 < 16; i0 += 8) {
-        uint4 v[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int r = 32 * warp + 2 * (i0 + i) + (lane >> 4), R = kTile * t + r;
-          const int q = u.r0 + R, token = q / G, head = h * G + q - token * G;
-          v[i] = R < u.rows ? ldg_cg_v4(a.q + (long long)(u.lo + token) * a.q_stride + (long long)head * kHeadDim + 8 * ch)
-                            : make_uint4(0, 0, 0, 0);
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int r = 32 * warp + 2 * (i0 + i) + (lane >> 4);
-          *reinterpret_cast<uint4*>(sq + (ch >> 3) * kHalf + r * 128 + (((ch & 7) ^ (r & 7)) << 4)) = v[i];
-        }
-      }
+      load_q(a, u, t, smem + t * kStageBytes, warp, lane);
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&C.q_full[t]);
     }
-    const int R = kTile * t + row, q = u.r0 + R;
-    const bool valid = R < u.rows;
-    const int lim = u.keys - u.n + q / G;  // last key that the row sees
-    const int lim0 = u.keys - u.n + (u.r0 + kTile * t + 32 * warp) / G;  // the warp's first row
     float m = neg_inf(), l = 0.0f;
     bool ok = true;
-    for (int j = k.t0; j < k.t1; ++j, ++n_tile) {
-      if (!wait(&C.s_full[t], n_s & 1, abort, a.status)) { ok = false; break; }
-      ++n_s;
-      tc::fence_after_sync();
-      uint32_t s[4][32];
+    {
+      const int G = a.nq / a.nkv, key0 = kTile * u.t0;
+      int lim = u.keys - u.n + (u.r0 + R) / G - key0;  // last key that the row sees, from the tile's start
+      int lim0 = u.keys - u.n + (u.r0 + kTile * t + 32 * warp) / G - key0;  // the warp's first row
+      for (int j = 0; j < nt; ++j, ++n_tile, lim -= kTile, lim0 -= kTile) {
+        if (!wait(&C.s_full[t], n_s & 1, abort, a.status)) { ok = false; break; }
+        ++n_s;
+        tc::fence_after_sync();
+        uint32_t s[4][32];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) tc::tmem_ld32_async(tS + 32 * i, s[i]);
-      tc::tmem_wait_ld();
+        for (int i = 0; i < 4; ++i) tc::tmem_ld32_async(tS + 32 * i, s[i]);
+        const TileInfo& info = C.info[n_tile % kInfo];
+        const int keys = info.keys;
+        const bool bad = info.some_bad[0] | info.some_bad[1];
+        tc::tmem_wait_ld();
 #pragma unroll
-      for (int i = 0; i < 4; ++i) tc::tmem_regs_ready(s[i]);
-      const TileInfo& info = C.info[n_tile % kInfo];
-      const int keys = info.keys;
-      const bool bad = (info.bad[0] | info.bad[1] | info.bad[2] | info.bad[3]) != 0;
-      if (keys < kTile || j * kTile + kTile - 1 > lim0) {
-        const int vis = min(keys, lim - j * kTile + 1);
+        for (int i = 0; i < 4; ++i) tc::tmem_regs_ready(s[i]);
+        if (keys < kTile || lim0 < kTile - 1) {
+          const int vis = min(keys, lim + 1);
 #pragma unroll
-        for (int i = 0; i < kTile; ++i)
-          if (i >= vis) s[i >> 5][i & 31] = 0xff800000u;
-      }
-      if (bad) {
-#pragma unroll
-        for (int i = 0; i < kTile; ++i) {
-          const int box = i >> p.box_log2;
-          if ((info.bad[box >> 5] >> (box & 31)) & 1u) s[i >> 5][i & 31] = 0xff800000u;
+          for (int i = 0; i < kTile; ++i)
+            if (i >= vis) s[i >> 5][i & 31] = 0xff800000u;
         }
-      }
-      float mx[4] = {neg_inf(), neg_inf(), neg_inf(), neg_inf()};
+        if (bad) {
 #pragma unroll
-      for (int i = 0; i < kTile; ++i) mx[i & 3] = fmaxf(mx[i & 3], __uint_as_float(s[i >> 5][i & 31]));
-      const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
-      const bool raise = mt > m + kLazy;
-      if (j > k.t0 && __any_sync(0xffffffffu, raise)) {
-        // S(j) was issued after PV(j - 1) and has completed, so O is stable
-        const float to = fmaxf(m, mt);
-        const float r = m == to ? 1.0f : ex2(m - to);
-        m = to;
-        l *= r;
+          for (int i = 0; i < kTile; ++i)
+            if ((info.bad[i >> 5] >> (i & 31)) & 1u) s[i >> 5][i & 31] = 0xff800000u;
+        }
+        float mx[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) mx[i] = fmaxf(__uint_as_float(s[i][0]), __uint_as_float(s[i][1]));
+#pragma unroll
+        for (int x = 2; x < 32; x += 2)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) mx[i] = max3(mx[i], __uint_as_float(s[i][x]), __uint_as_float(s[i][x + 1]));
+        const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
+        if (j == 0) {
+          m = mt;
+        } else if (__any_sync(0xffffffffu, mt > m + kLazy)) {
+          // S(j) was issued after PV(j - 1) and has completed, so O is stable
+          const float to = fmaxf(m, mt);
+          const float r = m == to ? 1.0f : ex2(m - to);
+          m = to;
+          l *= r;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            uint32_t o[16];
+            tc::tmem_ld16_async(tO + 16 * i, o);
+            tc::tmem_wait_ld();
+            tc::tmem_regs_ready16(o);
+#pragma unroll
+            for (int x = 0; x < 16; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * r);
+            tc::tmem_st16(tO + 16 * i, o);
+          }
+        }
+        const float neg = m == neg_inf() ? 0.0f : -m;
+        const unsigned long long c2 = pair(c, c), neg2 = pair(neg, neg);
+        unsigned long long sum[2] = {0ull, 0ull};
+        // 32 keys at a time: exponentials, sums, and P over S's first columns;
+        // the product may start on the first 64 keys while the rest follow
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          uint32_t o[32];
-          tc::tmem_ld32(tO + 32 * i, o);
+          uint32_t pk[16];
 #pragma unroll
-          for (int x = 0; x < 32; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * r);
-          tc::tmem_st32(tO + 32 * i, o);
+          for (int x = 0; x < 32; x += 2) {
+            float e0, e1;
+            unpair(fma2(pair(__uint_as_float(s[i][x]), __uint_as_float(s[i][x + 1])), c2, neg2), e0, e1);
+            e0 = ex2(e0);
+            e1 = ex2(e1);
+            sum[(x >> 1) & 1] = add2(sum[(x >> 1) & 1], pair(e0, e1));
+            pk[x >> 1] = pack2(e0, e1);
+          }
+          tc::tmem_st16(tS + 16 * i, pk);
+          if (i & 1) {
+            tc::tmem_wait_st();
+            tc::fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&C.p_full[t][i >> 1]);
+          }
         }
-      } else if (j == k.t0) {
-        m = mt;
+        float s0, s1;
+        unpair(add2(sum[0], sum[1]), s0, s1);
+        l += s0 + s1;
       }
-      const float neg = m == neg_inf() ? 0.0f : -m;
-      float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-#pragma unroll
-        for (int x = 0; x < 32; ++x) {
-          const float e = ex2(fmaf(__uint_as_float(s[i][x]), c, neg));
-          sum[x & 3] += e;
-          s[i][x] = __float_as_uint(e);
-        }
-      }
-      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-      uint32_t pk[2][32];
-#pragma unroll
-      for (int i = 0; i < 64; ++i)
-        pk[i >> 5][i & 31] = pack2(__uint_as_float(s[i >> 4][(2 * i) & 31]), __uint_as_float(s[i >> 4][(2 * i + 1) & 31]));
-      tc::tmem_st32(tS, pk[0]);
-      tc::tmem_st32(tS + 32, pk[1]);
-      tc::tmem_wait_st();
-      tc::fence_before_sync();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&C.p_full[t]);
     }
     if (!ok) break;
     if (nt > 0) {
@@ -433,12 +533,11 @@ FLINT_DEV void softmax_role(const Args& p, Ctl& C, uint8_t* smem, uint32_t tmem,
       ++n_o;
       tc::fence_after_sync();
     }
-    const int token = q / G, head = h * G + q - token * G;
-    const long long orow = (long long)(u.lo + token) * a.nq + head;
-    uint16_t* dst = a.out + orow * kHeadDim;
-    const bool whole = k.c_first == k.c_last;
+    const bool whole = u.c_first == u.c_last, valid = R < u.rows;
+    const long long row = out_row(a, u, R);
+    uint16_t* dst = a.out + row * kHeadDim;
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-    float* part = p.w.parts + (size_t)(2 * k.cta + (k.cta == k.c_first)) * kPartFloats;
+    float* part = part_of(p, u, blockIdx.x);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       uint32_t o[32];
@@ -463,236 +562,266 @@ FLINT_DEV void softmax_role(const Args& p, Ctl& C, uint8_t* smem, uint32_t tmem,
       if (lane == 0) mbar_arrive(&C.o_free[t]);
     }
     if (whole) {
-      if (valid && a.lse) a.lse[orow] = l == 0.0f ? neg_inf() : (m + log2f(l)) * 0.6931471805599453f;
-      continue;
-    }
-    part[kHeadDim * kUnitRows + R] = m;
-    part[(kHeadDim + 1) * kUnitRows + R] = l;
-    // the last of the unit's CTAs joins the parts
-    __threadfence();
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&C.wg[t]);
-    if (!wait(&C.wg[t], n_wg & 1, abort, a.status)) break;
-    ++n_wg;
-    if (warp == 0 && lane == 0) {
+      if (valid && a.lse) a.lse[row] = finish_lse(m, l);
+    } else {
+      part[kHeadDim * kUnitRows + R] = m;
+      part[(kHeadDim + 1) * kUnitRows + R] = l;
+      // the last of the unit's CTAs joins the parts
       __threadfence();
-      int* cnt = p.w.count + 2 * k.c_first + t;
-      const int last = atomicAdd(cnt, 1) == k.c_last - k.c_first;
-      if (last) *cnt = 0;
-      C.last[t] = last;
-      __threadfence();
-    }
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&C.wg[t]);
-    if (!wait(&C.wg[t], n_wg & 1, abort, a.status)) break;
-    ++n_wg;
-    if (!*reinterpret_cast<volatile int*>(&C.last[t])) continue;
-    __threadfence();
-    m = neg_inf();
-    for (int x = k.c_first; x <= k.c_last; ++x)
-      m = fmaxf(m, __ldcg(p.w.parts + (size_t)(2 * x + (x == k.c_first)) * kPartFloats + kHeadDim * kUnitRows + R));
-    l = 0.0f;
-    float o[4][32];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int x = 0; x < 32; ++x) o[i][x] = 0.0f;
-    for (int x = k.c_first; x <= k.c_last; ++x) {
-      const float* pp = p.w.parts + (size_t)(2 * x + (x == k.c_first)) * kPartFloats;
-      const float pm = __ldcg(pp + kHeadDim * kUnitRows + R), pl = __ldcg(pp + (kHeadDim + 1) * kUnitRows + R);
-      const float f = pm == neg_inf() ? (pl == 0.0f ? 0.0f : 1.0f) : ex2(pm - m);
-      l += f * pl;
-#pragma unroll
-      for (int i = 0; i < 32; ++i) {
-        const float4 v = __ldcg(reinterpret_cast<const float4*>(pp) + (size_t)i * kUnitRows + R);
-        o[i >> 3][4 * (i & 7)] += f * v.x;
-        o[i >> 3][4 * (i & 7) + 1] += f * v.y;
-        o[i >> 3][4 * (i & 7) + 2] += f * v.z;
-        o[i >> 3][4 * (i & 7) + 3] += f * v.w;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&C.wg[t]);
+      if (!wait(&C.wg[t], n_wg & 1, abort, a.status)) break;
+      ++n_wg;
+      if (warp == 0 && lane == 0) {
+        __threadfence();
+        int* cnt = p.w.count + 2 * u.c_first + t;
+        const int last = atomicAdd(cnt, 1) == u.c_last - u.c_first;
+        if (last) *cnt = 0;
+        C.last[t] = last;
+        __threadfence();
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&C.wg[t]);
+      if (!wait(&C.wg[t], n_wg & 1, abort, a.status)) break;
+      ++n_wg;
+      if (*reinterpret_cast<volatile int*>(&C.last[t])) {
+        __threadfence();
+        join_row(p, u, R);
       }
     }
-    if (valid) {
-      const float iv = l == 0.0f ? 0.0f : 1.0f / l;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) store_cols(dst + 32 * i, o[i], iv);
-      if (a.lse) a.lse[orow] = l == 0.0f ? neg_inf() : (m + log2f(l)) * 0.6931471805599453f;
-    }
+    piece_done(C, n);
   }
 }
 
 // ------------------------------------------------------------------ the MMAs
-FLINT_DEV void mma_role(const Args& p, Ctl& C, uint8_t* smem, uint32_t tmem) {
-  const int lane = threadIdx.x & 31;
+// The issue slots of this warp set the kernel's pace: descriptors are built
+// from warp-uniform values (uniform registers feed tcgen05.mma directly), of
+// which only the low words differ.
+FLINT_DEV uint32_t uniform(uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); }
+FLINT_DEV bool elect() {
+  uint32_t r;
+  asm volatile("{ .reg .pred p; elect.sync _|p, 0xffffffff; selp.u32 %0, 1, 0, p; }" : "=r"(r));
+  return r != 0;
+}
+FLINT_DEV uint64_t with_low(uint64_t desc, uint32_t low) { return (desc & 0xffffffff00000000ull) | low; }
+
+FLINT_DEV void mma_role(const Args& p, Ctl& C, uint8_t* smem, uint32_t tmem_any) {
   volatile int* abort = &C.abort;
   int* status = p.a.status;
   const uint32_t idS = tc::idesc_bf16(kTile, kTile), idO = idS | tc::kIdescBMajorN;
-  uint32_t it = 0, n_q[2] = {0, 0}, n_p[2] = {0, 0}, n_o[2] = {0, 0};
-  int n_tile = 0;
-  Walk k;
-  Entry u;
-  int h;
-  if (!walk_start(k, p)) return;
-  auto stage_wait = [&](uint32_t i) { return wait(&C.full[i % kStages], (i / kStages) & 1, abort, status); };
-  auto issue_s = [&](int t, uint32_t i) {  // S_t = Q_t K^T, K in ring slot i
-    if (lane == 0) {
-      const uint64_t dq = tc::desc_sw128(smem + t * kStageBytes);
-      const uint64_t dk = tc::desc_sw128(smem + kOffRing + (i % kStages) * kStageBytes);
+  const uint32_t tmem = uniform(tmem_any);
+  // descriptors of the ring's first stage; a stage adds kStageBytes / 16 to
+  // the low word (shared addresses stay below 2^18, inside its 14-bit field)
+  const uint64_t dk0 = tc::desc_sw128(smem + kOffRing), dv0 = tc::desc_sw128_mn(smem + kOffRing, kHalf);
+  const uint32_t q_low = uniform((uint32_t)tc::desc_sw128(smem));
+  const uint32_t k_low = uniform((uint32_t)dk0), v_low = uniform((uint32_t)dv0);
+  uint32_t st = 0, ph = 0;  // the next ring stage and its phase
+  uint32_t par_q = 0, par_p = 0, n_o = 0;  // parities by tile (bit t); units seen by tile (bit t)
+  uint32_t par_o = 0;
+  auto issue_s = [&](int t, uint32_t low) {  // S_t = Q_t K^T; K's descriptor low word
+    if (elect()) {
 #pragma unroll
       for (int kk = 0; kk < 8; ++kk) {
-        const uint64_t o = (uint64_t)((kk >> 2) * (kHalf >> 4) + 2 * (kk & 3));
-        tc::mma_bf16(tmem + (uint32_t)(kTile * t), dq + o, dk + o, idS, kk > 0);
+        const uint32_t o = (uint32_t)((kk >> 2) * (kHalf >> 4) + 2 * (kk & 3));
+        tc::mma_bf16(tmem + (uint32_t)(kTile * t), with_low(dk0, q_low + (uint32_t)(t * (kStageBytes >> 4)) + o),
+                     with_low(dk0, low + o), idS, kk > 0);
       }
       mbar_arrive(&C.s_full[t]);  // orders the tile's record before the softmax's reads
       tc::commit(&C.s_full[t]);
     }
     __syncwarp();
   };
-  while (!*abort && walk_next(k, u, h)) {
-    const int nt = k.t1 - k.t0;
-    if (nt == 0) continue;
-    const int tiles = u.rows > kTile ? 2 : 1;
-    // ring slots: it + 2 j is K_j, it + 2 j + 1 is V_j
-    bool ok = stage_wait(it);
-    for (int t = 0; ok && t < tiles; ++t) {
-      ok = wait(&C.q_full[t], n_q[t] & 1, abort, status);
-      if (!ok) break;
-      ++n_q[t];
-      tc::fence_after_sync();
-      issue_s(t, it);
-    }
-    if (!ok) break;
-    if (lane == 0) tc::commit(&C.empty[it % kStages]);
+  auto commit = [&](uint64_t* bar) {
+    if (elect()) tc::commit(bar);
     __syncwarp();
-    for (int j = 0; j < nt; ++j) {
-      const uint32_t iv = it + 2 * j + 1, ik = it + 2 * j + 2;
-      ok = stage_wait(iv);
-      if (!ok) break;
-      uint8_t* sv = smem + kOffRing + (iv % kStages) * kStageBytes;
-      const TileInfo& info = C.info[(n_tile + j) % kInfo];
-      if (info.keys < kTile || (info.bad[0] | info.bad[1] | info.bad[2] | info.bad[3]) != 0) {
-        // V rows that were not loaded, or past the sequence's end: zeros
-        for (int r = 0; r < kTile; ++r) {
-          const int box = r >> p.box_log2;
-          if (r >= info.keys || ((info.bad[box >> 5] >> (box & 31)) & 1u))
-            *reinterpret_cast<uint2*>(sv + (lane >> 4) * kHalf + r * 128 + (lane & 15) * 8) = make_uint2(0, 0);
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
+  };
+  for (uint32_t n = 0; piece_ready(C, n, status); ++n) {
+    const int nt = (int)uniform((uint32_t)(C.piece[n % kPieces].t1 - C.piece[n % kPieces].t0));
+    const int tiles = uniform((uint32_t)C.piece[n % kPieces].rows) > kTile ? 2 : 1;
+    piece_done(C, n);
+    if (nt == 0) continue;
+    auto next_stage = [&]() {
+      if (++st == kStages) {
+        st = 0;
+        ph ^= 1u;
       }
-      if (j + 1 < nt) {
-        ok = stage_wait(ik);
-        if (!ok) break;
-      }
-      for (int t = 0; t < tiles; ++t) {
-        ok = wait(&C.p_full[t], n_p[t] & 1, abort, status);
-        if (!ok) break;
-        ++n_p[t];
-        if (j == 0) {  // O_t of the CTA's previous unit has been read
-          if (n_o[t] > 0) ok = wait(&C.o_free[t], (n_o[t] - 1) & 1, abort, status);
-          if (!ok) break;
-          ++n_o[t];
-        }
-        tc::fence_after_sync();
-        if (lane == 0) {
-          const uint64_t dv = tc::desc_sw128_mn(sv, kHalf);
-#pragma unroll
-          for (int kk = 0; kk < 8; ++kk)
-            tc::mma_bf16_ta(tmem + (uint32_t)(2 * kTile + kTile * t), tmem + (uint32_t)(kTile * t + 8 * kk),
-                            dv + (uint64_t)(kk * (2048 >> 4)), idO, j > 0 || kk > 0);
-          if (j + 1 == nt) tc::commit(&C.o_full[t]);
-        }
-        __syncwarp();
-        if (j + 1 < nt) issue_s(t, ik);
-      }
-      if (!ok) break;
-      if (lane == 0) {
-        tc::commit(&C.empty[iv % kStages]);
-        if (j + 1 < nt) tc::commit(&C.empty[ik % kStages]);
-      }
-      __syncwarp();
+    };
+    // ring order K_0 V_0 K_1 V_1 ..
+    if (!wait(&C.full[st], ph, abort, status)) return;
+    const uint32_t first = uniform(st);
+    for (int t = 0; t < tiles; ++t) {
+      if (!wait(&C.q_full[t], (par_q >> t) & 1u, abort, status)) return;
+      par_q ^= 1u << t;
+      tc::fence_after_sync();
+      issue_s(t, k_low + first * (kStageBytes >> 4));
     }
-    if (!ok) break;
-    it += 2 * nt;
-    n_tile += nt;
+    commit(&C.empty[first]);
+    next_stage();
+    for (int j = 0; j < nt; ++j) {
+      const uint32_t sv = uniform(st);
+      if (!wait(&C.full[sv], ph, abort, status)) return;
+      next_stage();
+      const bool more = j + 1 < nt;
+      const uint32_t sk = uniform(st);
+      if (more && !wait(&C.full[sk], ph, abort, status)) return;
+      const uint32_t vl = v_low + sv * (kStageBytes >> 4), kl = k_low + sk * (kStageBytes >> 4);
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        if (t < tiles) {
+          if (j == 0) {  // O_t of the CTA's previous unit has been read
+            if (((n_o >> t) & 1u) && !wait(&C.o_free[t], (par_o >> t) & 1u, abort, status)) return;
+            if ((n_o >> t) & 1u) par_o ^= 1u << t;
+            n_o |= 1u << t;
+          }
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {  // keys 0 .. 63, 64 .. 127
+            if (!wait(&C.p_full[t][half], (par_p >> t) & 1u, abort, status)) return;
+            tc::fence_after_sync();
+            if (elect()) {
+#pragma unroll
+              for (int kk = 4 * half; kk < 4 * half + 4; ++kk)
+                tc::mma_bf16_ta(tmem + (uint32_t)(2 * kTile + kTile * t), tmem + (uint32_t)(kTile * t + 8 * kk),
+                                with_low(dv0, vl + (uint32_t)(kk * (2048 >> 4))), idO, j > 0 || kk > 0);
+            }
+            __syncwarp();
+          }
+          par_p ^= 1u << t;
+          if (more)
+            issue_s(t, kl);
+          else
+            commit(&C.o_full[t]);
+        }
+      }
+      commit(&C.empty[sv]);
+      if (more) {
+        commit(&C.empty[sk]);
+        next_stage();
+      }
+    }
   }
 }
 
 // ------------------------------------------------------------------ the loads
-FLINT_DEV void load_role(const Args& p, const Maps& maps, Ctl& C, uint8_t* smem) {
+// Keys (kv = 0) or values (kv = 1) of half a key tile (keys 64 part ..), by
+// 16-byte asynchronous copies, 16 lanes per key; what is not there (past the
+// sequence's end, or on a page outside the cache) is filled with zeros.  A
+// tile is handed over once the next one's copies are under way, or before
+// this warp has to wait.
+// PAGES16: pages of a multiple of 16 slots, so 16 keys from a multiple of 16
+// on lie at one stride; otherwise each key's place is looked up.
+template <bool PAGES16>
+FLINT_DEV void load_role(const Args& p, Ctl& C, uint8_t* smem, int kv, int part) {
   const AttnArgs& a = p.a;
-  const int lane = threadIdx.x & 31;
+  const int lane = threadIdx.x & 31, hi = lane >> 4, ch = lane & 15;
   volatile int* abort = &C.abort;
-  const int boxes = kTile / p.box;  // per tile: one lane each up to 32
-  uint32_t it = 0;
-  int n_tile = 0;
-  bool ok = true;
-  Walk k;
-  Entry u;
-  int h;
-  if (!walk_start(k, p)) return;
-  while (ok && !*abort && walk_next(k, u, h)) {
-    for (int j = k.t0; ok && j < k.t1; ++j, ++n_tile) {
-      const int key0 = j * kTile, keys = min(kTile, u.keys - key0);
-      // pages of this lane's boxes (lane + 32 x)
-      int page[4], slot[4];
-      uint32_t good[4];
-      TileInfo info;
-      info.keys = keys;
-      int n_good = 0;
+  const uint16_t* base = (kv ? a.v : a.k) + 8 * ch + (PAGES16 ? hi * a.s_slot : 0);
+  // where this lane's piece of key 2 i + hi goes, by i % 4
+  uint32_t to[4];
 #pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        const int box = lane + 32 * x, first = box * p.box;
-        const bool want = box < boxes && first < keys;
-        page[x] = 0;
-        slot[x] = 0;
-        bool in = false;
-        if (want) {
-          const int pos = key0 + first, blk = pos / a.block_size;
-          slot[x] = pos - blk * a.block_size;
-          page[x] = ldg_cg_i32(a.block_table + (long long)u.b * a.table_stride + blk);
-          in = page[x] >= 0 && page[x] < a.num_blocks;
-          if (!in) attn_error(a.status);
-        }
-        good[x] = __ballot_sync(0xffffffffu, in);
-        info.bad[x] = __ballot_sync(0xffffffffu, want && !in);
-        n_good += __popc(good[x]);
+  for (int q = 0; q < 4; ++q)
+    to[q] = (uint32_t)((ch >> 3) * kHalf + hi * 128 + (((ch & 7) ^ ((2 * q + hi) & 7)) << 4) + part * 64 * 128);
+  uint32_t st = (uint32_t)kv, ph = 0;  // ring slot and its use's parity
+  bool used = false;                   // whether the ring has gone round
+  int pending = -1;                    // slot whose copies are under way
+  int n_tile = 0;
+  auto hand_over = [&]() {
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&C.full[pending]);
+  };
+  auto flush = [&]() {
+    if (pending >= 0) {
+      cp_async_wait_all();
+      hand_over();
+      pending = -1;
+    }
+  };
+  // Offsets, -1 where there is none.  PAGES16: of the 16 keys from 16 (lane %
+  // 4) on; otherwise of keys lane and lane + 32 (of this warp's 64)
+  auto look_up = [&](const Piece& u, int key0, long long (&off)[2]) {
+    const int pos = key0 + 64 * part + (PAGES16 ? 16 * (lane & 3) : lane);
+    off[0] = pos < u.keys ? key_offset(a, u.b, pos) : -1;
+    if (!PAGES16) off[1] = pos + 32 < u.keys ? key_offset(a, u.b, pos + 32) : -1;
+  };
+  for (uint32_t n = 0;; ++n) {
+    if (!__all_sync(0xffffffffu, mbar_test_wait(&C.piece_full[n % kPieces], (n / kPieces) & 1))) flush();
+    if (!piece_ready(C, n, a.status)) break;
+    const Piece u = C.piece[n % kPieces];
+    piece_done(C, n);
+    const uint16_t* src = base + (long long)u.h * a.s_head;
+    long long off[2] = {-1, -1};
+    if (u.t0 < u.t1) look_up(u, u.t0 * kTile, off);
+    for (int j = u.t0; j < u.t1; ++j, ++n_tile) {
+      long long next[2] = {-1, -1};
+      if (j + 1 < u.t1) look_up(u, (j + 1) * kTile, next);
+      if (used) {
+        if (!__all_sync(0xffffffffu, mbar_test_wait(&C.empty[st], ph ^ 1u))) flush();
+        if (!wait(&C.empty[st], ph ^ 1u, abort, a.status)) break;
       }
-      const uint32_t bytes = (uint32_t)(n_good * p.box * 2 * 128);
-      for (int kv = 0; kv < 2; ++kv, ++it) {
-        const int s = it % kStages;
-        if (it >= (uint32_t)kStages) ok = wait(&C.empty[s], ((it / kStages) - 1) & 1, abort, a.status);
-        if (!ok) break;
-        if (lane == 0) {
-          if (kv == 0) C.info[n_tile % kInfo] = info;
-          mbar_arrive_expect_tx(&C.full[s], bytes);
+      const int keys = u.keys - j * kTile - 64 * part;  // of this warp's 64 (may be more, or none)
+      if (kv == 0) {
+        uint32_t b0, b1;
+        if (PAGES16) {
+          const uint32_t b = __ballot_sync(0xffffffffu, off[0] < 0 && 16 * (lane & 3) < keys);
+          b0 = (b & 1u ? 0xffffu : 0u) | (b & 2u ? 0xffff0000u : 0u);
+          b1 = (b & 4u ? 0xffffu : 0u) | (b & 8u ? 0xffff0000u : 0u);
+        } else {
+          b0 = __ballot_sync(0xffffffffu, off[0] < 0 && lane < keys);
+          b1 = __ballot_sync(0xffffffffu, off[1] < 0 && lane + 32 < keys);
         }
-        __syncwarp();
-        uint8_t* st = smem + kOffRing + s * kStageBytes;
-        const CUtensorMap* map = kv ? &maps.v : &maps.k;
+        if (lane == 0) {
+          TileInfo& info = C.info[n_tile % kInfo];
+          info.some_bad[part] = (b0 | b1) != 0;
+          info.bad[2 * part] = b0;
+          info.bad[2 * part + 1] = b1;
+          if (part == 0) info.keys = min(kTile, keys);
+        }
+      }
+      const uint32_t dst = smem_addr(smem + kOffRing + st * kStageBytes);
+      if (PAGES16) {
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
-          if ((good[x] >> lane) & 1u) {
-            uint8_t* dst = st + (lane + 32 * x) * p.box * 128;
-            tc::tma_load_4d(dst, map, 0, h, slot[x], page[x], &C.full[s]);
-            tc::tma_load_4d(dst + kHalf, map, 64, h, slot[x], page[x], &C.full[s]);
+          const long long o = __shfl_sync(0xffffffffu, off[0], x);
+          const uint16_t* from = src + (o < 0 ? 0 : o);
+          const int left = o < 0 ? 0 : keys - 16 * x - hi;  // keys from this lane's first on
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            cp_async16_or_zero(dst + (uint32_t)((8 * x + i) * 256) + to[i & 3], left > 2 * i ? from : src, left > 2 * i);
+            from += 2 * a.s_slot;
           }
         }
-        __syncwarp();
+      } else {
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const long long o = __shfl_sync(0xffffffffu, off[x], 2 * i + hi);
+            cp_async16_or_zero(dst + (uint32_t)((16 * x + i) * 256) + to[i & 3], src + (o < 0 ? 0 : o), o >= 0);
+          }
       }
-    }
-  }
-  if (*abort) {  // no copy may land after the block has exited
-    const uint32_t n = it < (uint32_t)kStages ? it : (uint32_t)kStages;
-    for (uint32_t i = it - n; i < it; ++i) {
-      const unsigned long long t0 = globaltimer_ns();
-      while (!mbar_test_wait(&C.full[i % kStages], (i / kStages) & 1) && globaltimer_ns() - t0 < kWaitNs) {
+      cp_async_commit();
+      if (pending >= 0) {
+        cp_async_wait_group<1>();
+        hand_over();
       }
+      pending = (int)st;
+      st += 2;
+      if (st >= (uint32_t)kStages) {
+        st -= (uint32_t)kStages;
+        used = true;
+        ph ^= 1u;
+      }
+      off[0] = next[0];
+      off[1] = next[1];
     }
+    if (*abort) break;
   }
+  flush();
+  cp_async_wait_all();  // no copy may land after the block has exited
 }
 
 __global__ void __launch_bounds__(kThreads, 1)
-    attn_prompt_kernel(const __grid_constant__ Args p, const __grid_constant__ Maps maps) {
+    attn_prompt_kernel(const __grid_constant__ Args p) {
   SpanGuard<kSpanAttnPrompt> span_guard;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
@@ -700,13 +829,18 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = threadIdx.x >> 5;
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
-      mbar_init(&C.full[i], 1);
+      mbar_init(&C.full[i], 2);
       mbar_init(&C.empty[i], 1);
+    }
+    for (int i = 0; i < kPieces; ++i) {
+      mbar_init(&C.piece_full[i], 1);
+      mbar_init(&C.piece_empty[i], kPieceReaders);
     }
     for (int t = 0; t < 2; ++t) {
       mbar_init(&C.q_full[t], 4);
       mbar_init(&C.s_full[t], 2);
-      mbar_init(&C.p_full[t], 4);
+      mbar_init(&C.p_full[t][0], 4);
+      mbar_init(&C.p_full[t][1], 4);
       mbar_init(&C.o_full[t], 1);
       mbar_init(&C.o_free[t], 4);
       mbar_init(&C.wg[t], 4);
@@ -728,8 +862,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
     if (warp == kWarpMma)
       mma_role(p, C, smem, tmem);
-    else if (warp == kWarpLoad)
-      load_role(p, maps, C, smem);
+    else if (warp == kWarpWalk)
+      walk_role(p, C);
+    else if (warp >= kWarpLoad) {
+      const int kv = (warp - kWarpLoad) & 1, part = (warp - kWarpLoad) >> 1;
+      if (p.a.block_size % 16 == 0)
+        load_role<true>(p, C, smem, kv, part);
+      else
+        load_role<false>(p, C, smem, kv, part);
+    }
   }
   tc::fence_before_sync();
   __syncthreads();
@@ -740,40 +881,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // --------------------------------------------------------------- host side
-PFN_cuTensorMapEncodeTiled_v12000 encoder() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
-    void* f = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) != cudaSuccess)
-      f = nullptr;
-    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
-  }();
-  return fn;
-}
-
-int box_rows(int page) {
-  int b = 1;
-  while (b < kTile && page % (2 * b) == 0) b *= 2;
-  return b;
-}
-
-bool make_map(CUtensorMap* m, const AttnArgs& a, const uint16_t* base, int box) {
-  auto fn = encoder();
-  if (!fn) return false;
-  const cuuint64_t dims[4] = {kHeadDim, (cuuint64_t)a.nkv, (cuuint64_t)a.block_size, (cuuint64_t)a.num_blocks};
-  // the stride of an extent of 1 is never used, but has to be a valid one
-  const cuuint64_t strides[3] = {(cuuint64_t)(a.nkv > 1 ? a.s_head * 2 : 256),
-                                 (cuuint64_t)(a.block_size > 1 ? a.s_slot * 2 : 256),
-                                 (cuuint64_t)(a.num_blocks > 1 ? a.s_block * 2 : 256)};
-  for (cuuint64_t s : strides)
-    if (s == 0 || s >= (1ull << 40)) return false;
-  const cuuint32_t bx[4] = {64, 1, (cuuint32_t)box, 1};
-  const cuuint32_t es[4] = {1, 1, 1, 1};
-  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<uint16_t*>(base), dims, strides, bx, es,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 }  // namespace
 
 PromptWs prompt_ws(void* base, int T, int B, int nq, int nkv) {
@@ -789,8 +896,7 @@ PromptWs prompt_ws(void* base, int T, int B, int nq, int nkv) {
   static_assert(kAttnPromptCounters + 2 * kPromptCtas * sizeof(int) <= kAttnData, "counters overlap");
   w.count = reinterpret_cast<int*>(b + kAttnPromptCounters);
   w.parts = reinterpret_cast<float*>(take((size_t)2 * kPromptCtas * kPartFloats * sizeof(float)));
-  w.starts = reinterpret_cast<int4*>(take((kPromptCtas + 1) * sizeof(int4)));
-  w.head = reinterpret_cast<long long*>(take(2 * sizeof(long long)));
+  w.starts = reinterpret_cast<int4*>(take(kPromptCtas * kStartWords * sizeof(int4)));
   w.first = reinterpret_cast<int*>(take((size_t)(B + 1) * sizeof(int)));
   w.entries = reinterpret_cast<int4*>(take(entries * 2 * sizeof(int4)));
   w.prefix = reinterpret_cast<long long*>(take((entries + 1) * sizeof(long long)));
@@ -802,10 +908,6 @@ cudaError_t launch_attn_prompt(const AttnArgs& a, const PromptWs& w, cudaStream_
   Args p;
   p.a = a;
   p.w = w;
-  p.box = box_rows(a.block_size);
-  for (p.box_log2 = 0; (1 << p.box_log2) < p.box;) ++p.box_log2;
-  Maps maps;
-  if (!make_map(&maps.k, a, a.k, p.box) || !make_map(&maps.v, a, a.v, p.box)) return cudaErrorNotSupported;
   int sms = 0;
   cudaError_t err = device_sms(&sms);
   if (err != cudaSuccess) return err;
@@ -836,7 +938,7 @@ cudaError_t launch_attn_prompt(const AttnArgs& a, const PromptWs& w, cudaStream_
   cfg.gridDim = dim3((unsigned)ctas);
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = kSmem;
-  void* args[] = {&p, &maps};
+  void* args[] = {&p};
   return cudaLaunchKernelExC(&cfg, fn, args);
 }
 

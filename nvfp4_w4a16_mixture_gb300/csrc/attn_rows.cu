@@ -311,7 +311,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1) attn_rows_kernel(const __grid
   auto fetch = [&](int slot) -> uint32_t {  // fills a slot; the mask of its valid keys
     uint32_t valid = 0;
     if (fmore) {
-      uint4* dst = ring + slot * (kChunkBytes / 16);
+      const uint32_t dst = smem_addr(ring + slot * (kChunkBytes / 16));
       valid = __ballot_sync(0xffffffffu, foff >= 0);
       const uint16_t* kb = a.k + (long long)f.h * a.s_head + 8 * t;
       const uint16_t* vb = a.v + (long long)f.h * a.s_head + 8 * g;
@@ -320,14 +320,14 @@ __global__ void __launch_bounds__(kRowsThreads, 1) attn_rows_kernel(const __grid
         const long long o = __shfl_sync(0xffffffffu, foff, g + 8 * e);
         const uint16_t* src = kb + (o < 0 ? 0 : o);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) cp_async16_or_zero(dst + 32 * (4 * e + i), src + 32 * i, o >= 0);
+        for (int i = 0; i < 4; ++i) cp_async16_or_zero(dst + 512 * (4 * e + i), src + 32 * i, o >= 0);
       }
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const long long o = __shfl_sync(0xffffffffu, foff, 2 * t + (e & 1) + 8 * (e >> 1));
         const uint16_t* src = vb + (o < 0 ? 0 : o);
 #pragma unroll
-        for (int i = 0; i < 2; ++i) cp_async16_or_zero(dst + 32 * (8 + 2 * e + i), src + 64 * i, o >= 0);
+        for (int i = 0; i < 2; ++i) cp_async16_or_zero(dst + 512 * (8 + 2 * e + i), src + 64 * i, o >= 0);
       }
       ++ftile;
       to_chunk();

@@ -266,9 +266,8 @@ FLINT_DEV void cp_async8(void* smem_dst, const void* gsrc) {
                : "memory");
 }
 // 16 bytes; zeros where `ok` is false (nothing is read then).
-FLINT_DEV void cp_async16_or_zero(void* smem_dst, const void* gsrc, bool ok) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(smem_dst)), "l"(gsrc),
-               "r"(ok ? 16 : 0)
+FLINT_DEV void cp_async16_or_zero(uint32_t smem_dst, const void* gsrc, bool ok) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_dst), "l"(gsrc), "r"(ok ? 16 : 0)
                : "memory");
 }
 FLINT_DEV void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }

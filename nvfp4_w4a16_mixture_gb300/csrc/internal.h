@@ -253,8 +253,7 @@ cudaError_t launch_attn_rows(const AttnArgs& a, const RowsWs& w, cudaStream_t st
 constexpr int kPromptCtas = 152;  // most CTAs of its grid (one per SM)
 struct PromptWs {
   int* count;            // [2 * kPromptCtas]: finished parts of a shared unit, zero between calls
-  int4* starts;          // [kPromptCtas + 1]: each CTA's first unit
-  long long* head;       // [2]: total weight, CTAs at work
+  int4* starts;          // [kPromptCtas, 4]: where each CTA's piece begins
   int* first;            // [B + 1]: first entry of each sequence
   int4* entries;         // [entries, 2]
   long long* prefix;     // [entries + 1]: weight before each entry
@@ -262,8 +261,6 @@ struct PromptWs {
   size_t total;
 };
 PromptWs prompt_ws(void* base, int T, int B, int nq, int nkv);
-// cudaErrorNotSupported, with nothing enqueued, for a cache whose strides no
-// tensor map takes.
 cudaError_t launch_attn_prompt(const AttnArgs& a, const PromptWs& w, cudaStream_t st);
 cudaError_t span_buffer_set_attn_prompt(unsigned long long* b);
 
