@@ -56,7 +56,7 @@ constexpr int kStageBytes = 2 * kHalf;
 constexpr int kStages = 5;
 constexpr int kOffRing = 2 * kStageBytes;  // after Q_0, Q_1
 constexpr int kOffCtl = kOffRing + kStages * kStageBytes;
-constexpr int kWarpMma = 8, kWarpWalk = 9, kWarpLoad = 12;  // 12 .. 15: K, V, K, V
+constexpr int kWarpMma = 8, kWarpWalk = 9, kWarpQ = 10, kWarpLoad = 12;  // two for Q, four for K, V, K, V
 constexpr int kThreads = 512;              // four warpgroups
 // Registers per thread: 128 at launch (65536 / 512); the two softmax
 // warpgroups take what the others give up: 2 * 200 + 2 * 56 = 4 * 128.
@@ -64,7 +64,7 @@ constexpr int kRegsLaunch = 128, kRegsSoftmax = 200, kRegsOther = 56;
 static_assert(2 * kRegsSoftmax + 2 * kRegsOther <= 4 * kRegsLaunch, "setmaxnreg.inc would wait for ever");
 constexpr int kInfo = 8;                   // key-tile records in flight
 constexpr int kPieces = 4;                 // pieces published ahead
-constexpr int kPieceReaders = 13;          // the softmax warps, the MMA and the load warps
+constexpr int kPieceReaders = 15;          // all warps but the walking one
 constexpr int kUnitWeight = 3;             // a unit's fixed part, in tile products
 constexpr int kMinWeight = 8;              // least work of a CTA
 constexpr float kLazy = 8.0f;
@@ -87,7 +87,7 @@ struct Piece {
 };
 struct Ctl {
   uint64_t full[kStages], empty[kStages];
-  uint64_t q_full[2], s_full[2], p_full[2][2], o_full[2], o_free[2], wg[2];
+  uint64_t q_full[2], q_free[2], s_full[2], p_full[2][2], o_full[2], o_free[2], wg[2];
   uint64_t piece_full[kPieces], piece_empty[kPieces];
   uint32_t tmem;
   int abort;
@@ -350,28 +350,6 @@ FLINT_DEV float finish_lse(float m, float l) {
   return l == 0.0f ? neg_inf() : (m + log2f(l)) * 0.6931471805599453f;
 }
 
-// Q rows of the piece's row tile t into swizzled shared memory, 16 lanes per
-// row.
-FLINT_DEV void load_q(const AttnArgs& a, const Piece& u, int t, uint8_t* sq, int warp, int lane) {
-  const int G = a.nq / a.nkv, ch = lane & 15;
-#pragma unroll
-  for (int i0 = 0; i0 < 16; i0 += 8) {
-    uint4 v[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int r = 32 * warp + 2 * (i0 + i) + (lane >> 4), R = kTile * t + r;
-      const int q = u.r0 + R, token = q / G, head = u.h * G + q - token * G;
-      v[i] = R < u.rows ? ldg_cg_v4(a.q + (long long)(u.lo + token) * a.q_stride + (long long)head * kHeadDim + 8 * ch)
-                        : make_uint4(0, 0, 0, 0);
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int r = 32 * warp + 2 * (i0 + i) + (lane >> 4);
-      *reinterpret_cast<uint4*>(sq + (ch >> 3) * kHalf + r * 128 + (((ch & 7) ^ (r & 7)) << 4)) = v[i];
-    }
-  }
-}
-
 // Row (of the output, in heads) of packed row R of the piece.
 FLINT_DEV long long out_row(const AttnArgs& a, const Piece& u, int R) {
   const int G = a.nq / a.nkv, q = u.r0 + R, token = q / G;
@@ -415,7 +393,7 @@ FLINT_DEV void join_row(const Args& p, const Piece& u, int R) {
   }
 }
 
-FLINT_DEV void softmax_role(const Args& p, Ctl& C, uint8_t* smem, uint32_t tmem, int t) {
+FLINT_DEV void softmax_role(const Args& p, Ctl& C, uint32_t tmem, int t) {
   const AttnArgs& a = p.a;
   const int warp = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31;
   const int R = kTile * t + 32 * warp + lane;  // packed row of the unit
@@ -433,12 +411,6 @@ FLINT_DEV void softmax_role(const Args& p, Ctl& C, uint8_t* smem, uint32_t tmem,
       n_tile += nt;
       piece_done(C, n);
       continue;
-    }
-    if (nt > 0) {
-      load_q(a, u, t, smem + t * kStageBytes, warp, lane);
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&C.q_full[t]);
     }
     float m = neg_inf(), l = 0.0f;
     bool ok = true;
@@ -618,7 +590,8 @@ FLINT_DEV void mma_role(const Args& p, Ctl& C, uint8_t* smem, uint32_t tmem_any)
   uint32_t st = 0, ph = 0;  // the next ring stage and its phase
   uint32_t par_q = 0, par_p = 0, n_o = 0;  // parities by tile (bit t); units seen by tile (bit t)
   uint32_t par_o = 0;
-  auto issue_s = [&](int t, uint32_t low) {  // S_t = Q_t K^T; K's descriptor low word
+  // S_t = Q_t K^T; K's descriptor low word; whether it is Q_t's last use
+  auto issue_s = [&](int t, uint32_t low, bool last) {
     if (elect()) {
 #pragma unroll
       for (int kk = 0; kk < 8; ++kk) {
@@ -628,6 +601,7 @@ FLINT_DEV void mma_role(const Args& p, Ctl& C, uint8_t* smem, uint32_t tmem_any)
       }
       mbar_arrive(&C.s_full[t]);  // orders the tile's record before the softmax's reads
       tc::commit(&C.s_full[t]);
+      if (last) tc::commit(&C.q_free[t]);
     }
     __syncwarp();
   };
@@ -653,7 +627,7 @@ FLINT_DEV void mma_role(const Args& p, Ctl& C, uint8_t* smem, uint32_t tmem_any)
       if (!wait(&C.q_full[t], (par_q >> t) & 1u, abort, status)) return;
       par_q ^= 1u << t;
       tc::fence_after_sync();
-      issue_s(t, k_low + first * (kStageBytes >> 4));
+      issue_s(t, k_low + first * (kStageBytes >> 4), nt == 1);
     }
     commit(&C.empty[first]);
     next_stage();
@@ -687,7 +661,7 @@ FLINT_DEV void mma_role(const Args& p, Ctl& C, uint8_t* smem, uint32_t tmem_any)
           }
           par_p ^= 1u << t;
           if (more)
-            issue_s(t, kl);
+            issue_s(t, kl, j + 2 == nt);
           else
             commit(&C.o_full[t]);
         }
@@ -702,6 +676,48 @@ FLINT_DEV void mma_role(const Args& p, Ctl& C, uint8_t* smem, uint32_t tmem_any)
 }
 
 // ------------------------------------------------------------------ the loads
+// Q's rows of row tile t, 16 lanes per row, as soon as the last product with
+// the previous unit's is done.
+FLINT_DEV void q_role(const Args& p, Ctl& C, uint8_t* smem, int t) {
+  const AttnArgs& a = p.a;
+  const int lane = threadIdx.x & 31, hi = lane >> 4, ch = lane & 15, G = a.nq / a.nkv;
+  const uint32_t dst = smem_addr(smem + t * kStageBytes) + (uint32_t)((ch >> 3) * kHalf + hi * 128);
+  uint32_t to[4];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) to[q] = dst + (uint32_t)(((ch & 7) ^ ((2 * q + hi) & 7)) << 4);
+  uint32_t used = 0;
+  for (uint32_t n = 0; piece_ready(C, n, a.status); ++n) {
+    const Piece& u = C.piece[n % kPieces];
+    const int rows = u.rows - kTile * t, nt = u.t1 - u.t0;
+    const int q = u.r0 + kTile * t + hi, token = q / G;
+    int head = q - token * G;
+    const uint16_t* from = a.q + (long long)(u.lo + token) * a.q_stride + (long long)(u.h * G + head) * kHeadDim + 8 * ch;
+    piece_done(C, n);
+    if (rows <= 0 || nt == 0) continue;
+    if (used > 0 && !wait(&C.q_free[t], (used - 1) & 1, &C.abort, a.status)) break;
+    ++used;
+    const long long wrap = a.q_stride - (long long)G * kHeadDim;
+    for (int i0 = 0; i0 < 64; i0 += 4) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const bool ok = 2 * (i0 + i) + hi < rows;
+        cp_async16_or_zero(to[i] + (uint32_t)((i0 + i) * 256), ok ? from : a.q, ok);
+        from += 2 * kHeadDim;  // two packed rows on
+        head += 2;
+        while (head >= G) {
+          head -= G;
+          from += wrap;
+        }
+      }
+    }
+    cp_async_commit();
+    cp_async_wait_all();
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&C.q_full[t]);
+  }
+}
+
 // Keys (kv = 0) or values (kv = 1) of half a key tile (keys 64 part ..), by
 // 16-byte asynchronous copies, 16 lanes per key; what is not there (past the
 // sequence's end, or on a page outside the cache) is filled with zeros.  A
@@ -837,7 +853,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&C.piece_empty[i], kPieceReaders);
     }
     for (int t = 0; t < 2; ++t) {
-      mbar_init(&C.q_full[t], 4);
+      mbar_init(&C.q_full[t], 1);
+      mbar_init(&C.q_free[t], 1);
       mbar_init(&C.s_full[t], 2);
       mbar_init(&C.p_full[t][0], 4);
       mbar_init(&C.p_full[t][1], 4);
@@ -857,14 +874,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   pdl_launch_dependents();
   if (warp < kWarpMma) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
-    softmax_role(p, C, smem, tmem, warp >> 2);
+    softmax_role(p, C, tmem, warp >> 2);
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
     if (warp == kWarpMma)
       mma_role(p, C, smem, tmem);
     else if (warp == kWarpWalk)
       walk_role(p, C);
-    else if (warp >= kWarpLoad) {
+    else if (warp < kWarpLoad)
+      q_role(p, C, smem, warp - kWarpQ);
+    else {
       const int kv = (warp - kWarpLoad) & 1, part = (warp - kWarpLoad) >> 1;
       if (p.a.block_size % 16 == 0)
         load_role<true>(p, C, smem, kv, part);
