@@ -43,6 +43,9 @@
 // become -inf, and their rows in shared memory are zeros (whatever the slots
 // hold).  Every wait is bounded (FLINT_ERR_TIMEOUT in the
 // status word on expiry).
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
 #include "attn.cuh"
 #include "tc.cuh"
 
@@ -56,7 +59,10 @@ constexpr int kStageBytes = 2 * kHalf;
 constexpr int kStages = 5;
 constexpr int kOffRing = 2 * kStageBytes;  // after Q_0, Q_1
 constexpr int kOffCtl = kOffRing + kStages * kStageBytes;
-constexpr int kWarpMma = 8, kWarpWalk = 9, kWarpQ = 10, kWarpLoad = 12;  // two for Q, four for K, V, K, V
+// A warp runs on scheduler warp % 4; the one that issues the MMAs shares its
+// own with no other busy warp than the two of the softmax.
+constexpr int kWarpMma = 8, kWarpIdle = 12, kWarpQ = 14, kWarpWalk = 15;
+constexpr int kWarpLoad = 9;               // 9 .. 11, 13: K, V, K, V
 constexpr int kThreads = 512;              // four warpgroups
 // Registers per thread: 128 at launch (65536 / 512); the two softmax
 // warpgroups take what the others give up: 2 * 200 + 2 * 56 = 4 * 128.
@@ -64,11 +70,11 @@ constexpr int kRegsLaunch = 128, kRegsSoftmax = 200, kRegsOther = 56;
 static_assert(2 * kRegsSoftmax + 2 * kRegsOther <= 4 * kRegsLaunch, "setmaxnreg.inc would wait for ever");
 constexpr int kInfo = 8;                   // key-tile records in flight
 constexpr int kPieces = 4;                 // pieces published ahead
-constexpr int kPieceReaders = 15;          // all warps but the walking one
+constexpr int kPieceReaders = 14;          // 8 softmax warps, MMA, Q, 4 loading ones
 constexpr int kUnitWeight = 3;             // a unit's fixed part, in tile products
 constexpr int kMinWeight = 8;              // least work of a CTA
 constexpr float kLazy = 8.0f;
-constexpr unsigned long long kWaitNs = 200ull * 1000 * 1000;
+constexpr uint32_t kWaitNs = 200u * 1000 * 1000;
 constexpr uint32_t kSuspendNs = 50000;
 constexpr int kPartFloats = kUnitRows * (kHeadDim + 2);
 
@@ -97,31 +103,64 @@ struct Ctl {
 };
 constexpr size_t kSmem = (size_t)kOffCtl + sizeof(Ctl) + 1024;
 
-// Called by a whole warp, with one answer for all its lanes.
-FLINT_DEV bool wait_lane(uint64_t* bar, uint32_t parity, volatile int* abort, int* status) {
-  if (mbar_test_wait(bar, parity)) return true;
-  unsigned long long t0 = 0;
-  for (;;) {
-    if (*abort) return false;
-    if (mbar_try_wait(bar, parity, kSuspendNs)) return true;
-    const unsigned long long now = globaltimer_ns();
-    if (t0 == 0) t0 = now;
-    if (now - t0 > kWaitNs) {
-      *abort = 1;
-      atomicCAS(status, 0, FLINT_ERR_TIMEOUT);
-      return false;
-    }
-  }
+// Barriers by their 32-bit shared-memory addresses.
+FLINT_DEV bool bar_test(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{ .reg .pred p; mbarrier.test_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
 }
+FLINT_DEV bool bar_try(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{ .reg .pred p; mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2, %3; selp.u32 %0, 1, 0, p; }"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity), "r"(kSuspendNs)
+      : "memory");
+  return ok != 0;
+}
+FLINT_DEV void bar_arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+FLINT_DEV void bar_expect(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.release.cta.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+FLINT_DEV void bar_commit(uint32_t bar) {  // once this thread's MMAs so far are done
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+FLINT_DEV bool aborted(const Ctl& C) { return *const_cast<const volatile int*>(&C.abort) != 0; }
 
-FLINT_DEV bool wait(uint64_t* bar, uint32_t parity, volatile int* abort, int* status) {
-  return __all_sync(0xffffffffu, wait_lane(bar, parity, abort, status));
+// Waits of a whole warp, with one answer for all its lanes.  What the warps of
+// this kernel run in turns has to fit the instruction caches, so the way taken
+// when the phase is not over yet is short and marked unlikely.
+FLINT_DEV bool is_over(uint32_t bar, uint32_t parity) { return __all_sync(0xffffffffu, bar_test(bar, parity)); }
+FLINT_DEV bool wait(uint32_t bar, uint32_t parity, Ctl& C, int* status) {
+  bool ok = is_over(bar, parity);
+  if (__builtin_expect(!ok, 0)) {
+    const uint32_t t0 = globaltimer_low();
+    while (!(ok = bar_try(bar, parity)) && !aborted(C)) {
+      if (globaltimer_low() - t0 > kWaitNs) {
+        *const_cast<volatile int*>(&C.abort) = 1;
+        atomicCAS(status, 0, FLINT_ERR_TIMEOUT);
+      }
+    }
+    ok = __all_sync(0xffffffffu, ok);
+  }
+  return ok;
 }
 
 struct Args {
   AttnArgs a;
   PromptWs w;
+  int box, box_log2;  // rows of a tiled copy: gcd(block_size, 128)
 };
+struct Maps {
+  CUtensorMap k, v;  // {128, heads, slots, pages}, box {64, 1, box, 1}
+};
+constexpr int kMinBox = 4;  // smallest box worth a tiled copy: 32 per key tile and half
 
 // ---------------------------------------------------------------- the plan
 // A CTA's start record: {entry, kv head, offset in the unit, CTAs at work},
@@ -245,7 +284,6 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const Args p, i
 // units on it, a few ahead of their use.
 FLINT_DEV void walk_role(const Args& p, Ctl& C) {
   const int lane = threadIdx.x & 31, cta = blockIdx.x, nkv = p.a.nkv;
-  volatile int* abort = &C.abort;
   const int4* start = p.w.starts + kStartWords * cta;
   const uint4 s0 = ldg_cg_v4(start), s1 = ldg_cg_v4(start + 1);
   Entry e = load_entry(start + 2);
@@ -254,11 +292,11 @@ FLINT_DEV void walk_role(const Args& p, Ctl& C) {
   long long rem = ctas == 0 ? 0 : (long long)((unsigned long long)s1.w << 32 | s1.z);
   uint32_t n = 0;
   auto publish = [&](const Piece& x) {
-    if (n >= (uint32_t)kPieces && !wait(&C.piece_empty[n % kPieces], ((n / kPieces) - 1) & 1, abort, p.a.status))
+    if (n >= (uint32_t)kPieces && !wait(smem_addr(&C.piece_empty[n % kPieces]), ((n / kPieces) - 1) & 1, C, p.a.status))
       return false;
     if (lane == 0) {
       C.piece[n % kPieces] = x;
-      mbar_arrive(&C.piece_full[n % kPieces]);
+      bar_arrive(smem_addr(&C.piece_full[n % kPieces]));
     }
     __syncwarp();
     ++n;
@@ -300,12 +338,12 @@ FLINT_DEV void walk_role(const Args& p, Ctl& C) {
 
 // Piece n, once it is published; false at the end (or on expiry).
 FLINT_DEV bool piece_ready(Ctl& C, uint32_t n, int* status) {
-  return wait(&C.piece_full[n % kPieces], (n / kPieces) & 1, &C.abort, status) && C.piece[n % kPieces].valid;
+  return wait(smem_addr(&C.piece_full[n % kPieces]), (n / kPieces) & 1, C, status) && C.piece[n % kPieces].valid;
 }
 // This warp has read all it needs of piece n.
 FLINT_DEV void piece_done(Ctl& C, uint32_t n) {
   __syncwarp();
-  if ((threadIdx.x & 31) == 0) mbar_arrive(&C.piece_empty[n % kPieces]);
+  if ((threadIdx.x & 31) == 0) bar_arrive(smem_addr(&C.piece_empty[n % kPieces]));
 }
 
 FLINT_DEV uint32_t pack2(float a, float b) {
@@ -393,7 +431,8 @@ FLINT_DEV void join_row(const Args& p, const Piece& u, int R) {
   }
 }
 
-FLINT_DEV void softmax_role(const Args& p, Ctl& C, uint32_t tmem, int t) {
+template <bool TILED>
+FLINT_DEV void softmax_role(const Args& p, Ctl& C, uint8_t* smem, uint32_t tmem, int t) {
   const AttnArgs& a = p.a;
   const int warp = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31;
   const int R = kTile * t + 32 * warp + lane;  // packed row of the unit
@@ -401,7 +440,6 @@ FLINT_DEV void softmax_role(const Args& p, Ctl& C, uint32_t tmem, int t) {
   const uint32_t tS = tmem + lanes + (uint32_t)(kTile * t);
   const uint32_t tO = tmem + lanes + (uint32_t)(2 * kTile + kTile * t);
   const float c = a.scale * 1.4426950408889634f;
-  volatile int* abort = &C.abort;
   uint32_t n_s = 0, n_o = 0, n_wg = 0;  // phases done: s_full, o_full, wg
   int n_tile = 0;                       // key tiles of the CTA so far
   for (uint32_t n = 0; piece_ready(C, n, a.status); ++n) {
@@ -419,7 +457,7 @@ FLINT_DEV void softmax_role(const Args& p, Ctl& C, uint32_t tmem, int t) {
       int lim = u.keys - u.n + (u.r0 + R) / G - key0;  // last key that the row sees, from the tile's start
       int lim0 = u.keys - u.n + (u.r0 + kTile * t + 32 * warp) / G - key0;  // the warp's first row
       for (int j = 0; j < nt; ++j, ++n_tile, lim -= kTile, lim0 -= kTile) {
-        if (!wait(&C.s_full[t], n_s & 1, abort, a.status)) { ok = false; break; }
+        if (!wait(smem_addr(&C.s_full[t]), n_s & 1, C, a.status)) { ok = false; break; }
         ++n_s;
         tc::fence_after_sync();
         uint32_t s[4][32];
@@ -437,63 +475,94 @@ FLINT_DEV void softmax_role(const Args& p, Ctl& C, uint32_t tmem, int t) {
           for (int i = 0; i < kTile; ++i)
             if (i >= vis) s[i >> 5][i & 31] = 0xff800000u;
         }
+        if (TILED && (keys < kTile || bad)) {
+          // V's rows past the sequence's end or not loaded: zeros, whatever the
+          // slots hold (P is 0 there).  V_j is in ring slot 2 n_tile + 1
+          const uint32_t i = 2 * (uint32_t)n_tile + 1, r = (uint32_t)(32 * warp + lane);
+          if (!wait(smem_addr(&C.full[i % kStages]), (i / kStages) & 1u, C, a.status)) { ok = false; break; }
+          if ((int)r >= keys || (bad && ((info.bad[r >> 5] >> (r & 31)) & 1u))) {
+            uint4* v = reinterpret_cast<uint4*>(smem + kOffRing + (i % kStages) * kStageBytes + r * 128);
+#pragma unroll 1
+            for (int x = 0; x < 8; ++x) v[x] = v[x + kHalf / 16] = make_uint4(0, 0, 0, 0);
+          }
+          fence_proxy_async_smem();
+        }
         if (bad) {
 #pragma unroll
           for (int i = 0; i < kTile; ++i)
             if ((info.bad[i >> 5] >> (i & 31)) & 1u) s[i >> 5][i & 31] = 0xff800000u;
         }
-        float mx[4];
+        // P of the first 64 keys against the reference so far, and beside it
+        // (other units of the SM) the tile's maximum
+        float mx[4] = {neg_inf(), neg_inf(), neg_inf(), neg_inf()};
+        uint32_t pk[32];
+        unsigned long long sum[2] = {0ull, 0ull};
+        const unsigned long long c2 = pair(c, c);
+        auto exps = [&](int i, int x, uint32_t& out, unsigned long long neg2) {  // keys 32 i + x, + 1
+          float e0, e1;
+          unpair(fma2(pair(__uint_as_float(s[i][x]), __uint_as_float(s[i][x + 1])), c2, neg2), e0, e1);
+          e0 = ex2(e0);
+          e1 = ex2(e1);
+          sum[(x >> 1) & 1] = add2(sum[(x >> 1) & 1], pair(e0, e1));
+          out = pack2(e0, e1);
+        };
+        auto reference = [&]() {
+          const float neg = m == neg_inf() ? 0.0f : -m;
+          return pair(neg, neg);
+        };
+        unsigned long long neg2 = reference();
 #pragma unroll
-        for (int i = 0; i < 4; ++i) mx[i] = fmaxf(__uint_as_float(s[i][0]), __uint_as_float(s[i][1]));
+        for (int x = 0; x < 32; x += 2) {
 #pragma unroll
-        for (int x = 2; x < 32; x += 2)
+          for (int i = 0; i < 2; ++i) exps(i, x, pk[16 * i + (x >> 1)], neg2);
 #pragma unroll
           for (int i = 0; i < 4; ++i) mx[i] = max3(mx[i], __uint_as_float(s[i][x]), __uint_as_float(s[i][x + 1]));
+        }
         const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
-        if (j == 0) {
-          m = mt;
-        } else if (__any_sync(0xffffffffu, mt > m + kLazy)) {
-          // S(j) was issued after PV(j - 1) and has completed, so O is stable
+        if (__any_sync(0xffffffffu, mt > m + kLazy)) {
+          // the reference moves: the first tile, and now and then later.  S(j)
+          // was issued after PV(j - 1) and has completed, so O is stable
           const float to = fmaxf(m, mt);
           const float r = m == to ? 1.0f : ex2(m - to);
           m = to;
           l *= r;
+          if (j > 0) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            uint32_t o[16];
-            tc::tmem_ld16_async(tO + 16 * i, o);
-            tc::tmem_wait_ld();
-            tc::tmem_regs_ready16(o);
+            for (int i = 0; i < 8; ++i) {
+              uint32_t o[16];
+              tc::tmem_ld16_async(tO + 16 * i, o);
+              tc::tmem_wait_ld();
+              tc::tmem_regs_ready16(o);
 #pragma unroll
-            for (int x = 0; x < 16; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * r);
-            tc::tmem_st16(tO + 16 * i, o);
+              for (int x = 0; x < 16; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * r);
+              tc::tmem_st16(tO + 16 * i, o);
+            }
           }
+          neg2 = reference();
+          sum[0] = sum[1] = 0ull;
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int x = 0; x < 32; x += 2) exps(i, x, pk[16 * i + (x >> 1)], neg2);
         }
-        const float neg = m == neg_inf() ? 0.0f : -m;
-        const unsigned long long c2 = pair(c, c), neg2 = pair(neg, neg);
-        unsigned long long sum[2] = {0ull, 0ull};
-        // 32 keys at a time: exponentials, sums, and P over S's first columns;
-        // the product may start on the first 64 keys while the rest follow
+        // P over S's first columns; its product starts on the first 64 keys
+        // while the rest follow
+        auto hand_over = [&](int half) {
+          tc::tmem_wait_st();
+          tc::fence_before_sync();
+          __syncwarp();
+          if (lane == 0) bar_arrive(smem_addr(&C.p_full[t][half]));
+        };
+        tc::tmem_st16(tS, pk);
+        tc::tmem_st16(tS + 16, pk + 16);
+        hand_over(0);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          uint32_t pk[16];
+        for (int i = 2; i < 4; ++i) {
 #pragma unroll
-          for (int x = 0; x < 32; x += 2) {
-            float e0, e1;
-            unpair(fma2(pair(__uint_as_float(s[i][x]), __uint_as_float(s[i][x + 1])), c2, neg2), e0, e1);
-            e0 = ex2(e0);
-            e1 = ex2(e1);
-            sum[(x >> 1) & 1] = add2(sum[(x >> 1) & 1], pair(e0, e1));
-            pk[x >> 1] = pack2(e0, e1);
-          }
+          for (int x = 0; x < 32; x += 2) exps(i, x, pk[x >> 1], neg2);
           tc::tmem_st16(tS + 16 * i, pk);
-          if (i & 1) {
-            tc::tmem_wait_st();
-            tc::fence_before_sync();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&C.p_full[t][i >> 1]);
-          }
         }
+        hand_over(1);
         float s0, s1;
         unpair(add2(sum[0], sum[1]), s0, s1);
         l += s0 + s1;
@@ -501,7 +570,7 @@ FLINT_DEV void softmax_role(const Args& p, Ctl& C, uint32_t tmem, int t) {
     }
     if (!ok) break;
     if (nt > 0) {
-      if (!wait(&C.o_full[t], n_o & 1, abort, a.status)) break;
+      if (!wait(smem_addr(&C.o_full[t]), n_o & 1, C, a.status)) break;
       ++n_o;
       tc::fence_after_sync();
     }
@@ -531,7 +600,7 @@ FLINT_DEV void softmax_role(const Args& p, Ctl& C, uint32_t tmem, int t) {
     if (nt > 0) {
       tc::fence_before_sync();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&C.o_free[t]);
+      if (lane == 0) bar_arrive(smem_addr(&C.o_free[t]));
     }
     if (whole) {
       if (valid && a.lse) a.lse[row] = finish_lse(m, l);
@@ -541,8 +610,8 @@ FLINT_DEV void softmax_role(const Args& p, Ctl& C, uint32_t tmem, int t) {
       // the last of the unit's CTAs joins the parts
       __threadfence();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&C.wg[t]);
-      if (!wait(&C.wg[t], n_wg & 1, abort, a.status)) break;
+      if (lane == 0) bar_arrive(smem_addr(&C.wg[t]));
+      if (!wait(smem_addr(&C.wg[t]), n_wg & 1, C, a.status)) break;
       ++n_wg;
       if (warp == 0 && lane == 0) {
         __threadfence();
@@ -553,8 +622,8 @@ FLINT_DEV void softmax_role(const Args& p, Ctl& C, uint32_t tmem, int t) {
         __threadfence();
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(&C.wg[t]);
-      if (!wait(&C.wg[t], n_wg & 1, abort, a.status)) break;
+      if (lane == 0) bar_arrive(smem_addr(&C.wg[t]));
+      if (!wait(smem_addr(&C.wg[t]), n_wg & 1, C, a.status)) break;
       ++n_wg;
       if (*reinterpret_cast<volatile int*>(&C.last[t])) {
         __threadfence();
@@ -578,7 +647,6 @@ FLINT_DEV bool elect() {
 FLINT_DEV uint64_t with_low(uint64_t desc, uint32_t low) { return (desc & 0xffffffff00000000ull) | low; }
 
 FLINT_DEV void mma_role(const Args& p, Ctl& C, uint8_t* smem, uint32_t tmem_any) {
-  volatile int* abort = &C.abort;
   int* status = p.a.status;
   const uint32_t idS = tc::idesc_bf16(kTile, kTile), idO = idS | tc::kIdescBMajorN;
   const uint32_t tmem = uniform(tmem_any);
@@ -587,26 +655,30 @@ FLINT_DEV void mma_role(const Args& p, Ctl& C, uint8_t* smem, uint32_t tmem_any)
   const uint64_t dk0 = tc::desc_sw128(smem + kOffRing), dv0 = tc::desc_sw128_mn(smem + kOffRing, kHalf);
   const uint32_t q_low = uniform((uint32_t)tc::desc_sw128(smem));
   const uint32_t k_low = uniform((uint32_t)dk0), v_low = uniform((uint32_t)dv0);
-  uint32_t st = 0, ph = 0;  // the next ring stage and its phase
-  uint32_t par_q = 0, par_p = 0, n_o = 0;  // parities by tile (bit t); units seen by tile (bit t)
-  uint32_t par_o = 0;
-  // S_t = Q_t K^T; K's descriptor low word; whether it is Q_t's last use
-  auto issue_s = [&](int t, uint32_t low, bool last) {
+  uint32_t st = 0, ph = 0;                 // the next ring stage and its phase
+  uint32_t par_q = 0, par_p = 0, par_o = 0;  // parities by tile (bit t)
+  uint32_t had = 0;                        // tiles that have had a unit (bit t)
+  auto next_stage = [&]() {
+    if (++st == kStages) {
+      st = 0;
+      ph ^= 1u;
+    }
+  };
+  // S_t = Q_t K^T, K in stage sk; whether it is Q_t's last use, and K's
+  auto issue_s = [&](int t, uint32_t sk, bool last_q, bool last_k) {
     if (elect()) {
+      const uint32_t low = k_low + sk * (kStageBytes >> 4);
 #pragma unroll
       for (int kk = 0; kk < 8; ++kk) {
         const uint32_t o = (uint32_t)((kk >> 2) * (kHalf >> 4) + 2 * (kk & 3));
         tc::mma_bf16(tmem + (uint32_t)(kTile * t), with_low(dk0, q_low + (uint32_t)(t * (kStageBytes >> 4)) + o),
                      with_low(dk0, low + o), idS, kk > 0);
       }
-      mbar_arrive(&C.s_full[t]);  // orders the tile's record before the softmax's reads
-      tc::commit(&C.s_full[t]);
-      if (last) tc::commit(&C.q_free[t]);
+      bar_arrive(smem_addr(&C.s_full[t]));  // orders the tile's record before the softmax's reads
+      bar_commit(smem_addr(&C.s_full[t]));
+      if (last_q) bar_commit(smem_addr(&C.q_free[t]));
+      if (last_k) bar_commit(smem_addr(&C.empty[sk]));
     }
-    __syncwarp();
-  };
-  auto commit = [&](uint64_t* bar) {
-    if (elect()) tc::commit(bar);
     __syncwarp();
   };
   for (uint32_t n = 0; piece_ready(C, n, status); ++n) {
@@ -614,107 +686,196 @@ FLINT_DEV void mma_role(const Args& p, Ctl& C, uint8_t* smem, uint32_t tmem_any)
     const int tiles = uniform((uint32_t)C.piece[n % kPieces].rows) > kTile ? 2 : 1;
     piece_done(C, n);
     if (nt == 0) continue;
-    auto next_stage = [&]() {
-      if (++st == kStages) {
-        st = 0;
-        ph ^= 1u;
-      }
-    };
     // ring order K_0 V_0 K_1 V_1 ..
-    if (!wait(&C.full[st], ph, abort, status)) return;
+    if (!wait(smem_addr(&C.full[st]), ph, C, status)) return;
     const uint32_t first = uniform(st);
+#pragma unroll 1
     for (int t = 0; t < tiles; ++t) {
-      if (!wait(&C.q_full[t], (par_q >> t) & 1u, abort, status)) return;
+      if (!wait(smem_addr(&C.q_full[t]), (par_q >> t) & 1u, C, status)) return;
       par_q ^= 1u << t;
       tc::fence_after_sync();
-      issue_s(t, k_low + first * (kStageBytes >> 4), nt == 1);
+      issue_s(t, first, nt == 1, t + 1 == tiles);
     }
-    commit(&C.empty[first]);
     next_stage();
+    bool has_v = false, has_k = false;  // whether V_j, K_j+1 are known to be there
     for (int j = 0; j < nt; ++j) {
-      const uint32_t sv = uniform(st);
-      if (!wait(&C.full[sv], ph, abort, status)) return;
-      next_stage();
       const bool more = j + 1 < nt;
+      const uint32_t sv = uniform(st);
+      if (!has_v && !wait(smem_addr(&C.full[sv]), ph, C, status)) return;
+      next_stage();
       const uint32_t sk = uniform(st);
-      if (more && !wait(&C.full[sk], ph, abort, status)) return;
-      const uint32_t vl = v_low + sv * (kStageBytes >> 4), kl = k_low + sk * (kStageBytes >> 4);
+      if (more) {
+        if (!has_k && !wait(smem_addr(&C.full[sk]), ph, C, status)) return;
+        next_stage();
+      }
+      has_v = has_k = false;
+      // (unrolled: a straight run of code is what the instruction fetch keeps
+      // up with)
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
-        if (t < tiles) {
+        if (t == 0 || tiles == 2) {
           if (j == 0) {  // O_t of the CTA's previous unit has been read
-            if (((n_o >> t) & 1u) && !wait(&C.o_free[t], (par_o >> t) & 1u, abort, status)) return;
-            if ((n_o >> t) & 1u) par_o ^= 1u << t;
-            n_o |= 1u << t;
+            if ((had >> t) & 1u) {
+              if (!wait(smem_addr(&C.o_free[t]), (par_o >> t) & 1u, C, status)) return;
+              par_o ^= 1u << t;
+            }
+            had |= 1u << t;
           }
+          const bool last = t + 1 == tiles;
 #pragma unroll
           for (int half = 0; half < 2; ++half) {  // keys 0 .. 63, 64 .. 127
-            if (!wait(&C.p_full[t][half], (par_p >> t) & 1u, abort, status)) return;
+            if (!wait(smem_addr(&C.p_full[t][half]), (par_p >> t) & 1u, C, status)) return;
             tc::fence_after_sync();
             if (elect()) {
+              const uint32_t low = v_low + sv * (kStageBytes >> 4);
 #pragma unroll
               for (int kk = 4 * half; kk < 4 * half + 4; ++kk)
                 tc::mma_bf16_ta(tmem + (uint32_t)(2 * kTile + kTile * t), tmem + (uint32_t)(kTile * t + 8 * kk),
-                                with_low(dv0, vl + (uint32_t)(kk * (2048 >> 4))), idO, j > 0 || kk > 0);
+                                with_low(dv0, low + (uint32_t)(kk * (2048 >> 4))), idO, j > 0 || kk > 0);
+              if (half == 1) {
+                if (last) bar_commit(smem_addr(&C.empty[sv]));
+                if (!more) bar_commit(smem_addr(&C.o_full[t]));
+              }
             }
             __syncwarp();
+            // while products run: is the next K there already?
+            if (t == 1 && half == 0 && j + 2 < nt)
+              has_k = is_over(smem_addr(&C.full[st + 1 == kStages ? 0 : st + 1]), st + 1 == kStages ? ph ^ 1u : ph);
           }
           par_p ^= 1u << t;
-          if (more)
-            issue_s(t, kl, j + 2 == nt);
-          else
-            commit(&C.o_full[t]);
+          if (more) issue_s(t, sk, j + 2 == nt, last);
+          if (t == 0 && more) has_v = is_over(smem_addr(&C.full[st]), ph);  // the next V?
         }
-      }
-      commit(&C.empty[sv]);
-      if (more) {
-        commit(&C.empty[sk]);
-        next_stage();
       }
     }
   }
 }
 
 // ------------------------------------------------------------------ the loads
-// Q's rows of row tile t, 16 lanes per row, as soon as the last product with
+// Q's rows, 16 lanes per row, each row tile as soon as the last product with
 // the previous unit's is done.
-FLINT_DEV void q_role(const Args& p, Ctl& C, uint8_t* smem, int t) {
+FLINT_DEV void q_role(const Args& p, Ctl& C, uint8_t* smem) {
   const AttnArgs& a = p.a;
   const int lane = threadIdx.x & 31, hi = lane >> 4, ch = lane & 15, G = a.nq / a.nkv;
-  const uint32_t dst = smem_addr(smem + t * kStageBytes) + (uint32_t)((ch >> 3) * kHalf + hi * 128);
   uint32_t to[4];
 #pragma unroll
-  for (int q = 0; q < 4; ++q) to[q] = dst + (uint32_t)(((ch & 7) ^ ((2 * q + hi) & 7)) << 4);
-  uint32_t used = 0;
+  for (int q = 0; q < 4; ++q)
+    to[q] = smem_addr(smem) + (uint32_t)((ch >> 3) * kHalf + hi * 128 + (((ch & 7) ^ ((2 * q + hi) & 7)) << 4));
+  const long long wrap = a.q_stride - (long long)G * kHeadDim;  // from a token's group to the next token's
+  uint32_t used[2] = {0, 0};
   for (uint32_t n = 0; piece_ready(C, n, a.status); ++n) {
     const Piece& u = C.piece[n % kPieces];
-    const int rows = u.rows - kTile * t, nt = u.t1 - u.t0;
-    const int q = u.r0 + kTile * t + hi, token = q / G;
+    const int rows = u.rows, nt = u.t1 - u.t0;
+    const int q = u.r0 + hi, token = q / G;
     int head = q - token * G;
     const uint16_t* from = a.q + (long long)(u.lo + token) * a.q_stride + (long long)(u.h * G + head) * kHeadDim + 8 * ch;
     piece_done(C, n);
-    if (rows <= 0 || nt == 0) continue;
-    if (used > 0 && !wait(&C.q_free[t], (used - 1) & 1, &C.abort, a.status)) break;
-    ++used;
-    const long long wrap = a.q_stride - (long long)G * kHeadDim;
-    for (int i0 = 0; i0 < 64; i0 += 4) {
+    if (nt == 0) continue;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const bool ok = 2 * (i0 + i) + hi < rows;
-        cp_async16_or_zero(to[i] + (uint32_t)((i0 + i) * 256), ok ? from : a.q, ok);
-        from += 2 * kHeadDim;  // two packed rows on
-        head += 2;
-        while (head >= G) {
-          head -= G;
-          from += wrap;
+    for (int t = 0; t < 2; ++t) {
+      if (rows <= kTile * t) break;
+      if (used[t] > 0 && !wait(smem_addr(&C.q_free[t]), (used[t] - 1) & 1, C, a.status)) return;
+      ++used[t];
+      for (int i0 = 0; i0 < 64; i0 += 4) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const bool ok = kTile * t + 2 * (i0 + i) + hi < rows;
+          cp_async16_or_zero(to[i] + (uint32_t)(t * kStageBytes + (i0 + i) * 256), ok ? from : a.q, ok);
+          from += 2 * kHeadDim;  // two packed rows on
+          head += 2;
+          while (head >= G) {
+            head -= G;
+            from += wrap;
+          }
         }
       }
+      cp_async_commit();
+      cp_async_wait_all();
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) bar_arrive(smem_addr(&C.q_full[t]));
     }
-    cp_async_commit();
-    cp_async_wait_all();
-    fence_proxy_async_smem();
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&C.q_full[t]);
+  }
+}
+
+// Keys (kv = 0) or values (kv = 1) of the key tiles, dims 64 half .. + 63, by
+// tiled copies of `box` slots of a page, one per lane.  (One warp issues a box
+// in about 80 cycles whatever its size, four warps on four schedulers a pair
+// of 32 KB tiles of 16-slot boxes in about 1100 cycles; the products take
+// 2048.)
+FLINT_DEV void load_tiled_role(const Args& p, const Maps& maps, Ctl& C, uint8_t* smem, int kv, int half) {
+  const AttnArgs& a = p.a;
+  const int lane = threadIdx.x & 31, boxes = kTile >> p.box_log2;
+  const CUtensorMap* map = kv ? &maps.v : &maps.k;
+  uint32_t st = (uint32_t)kv, ph = 0, uses = 0;
+  int n_tile = 0;
+  bool used = false, ok = true;
+  for (uint32_t n = 0; ok && piece_ready(C, n, a.status); ++n) {
+    const Piece& u = C.piece[n % kPieces];
+    const int b = u.b, h = u.h, keys_all = u.keys, t0 = u.t0, t1 = u.t1;
+    piece_done(C, n);
+    // page and slot of this lane's box of the tile at key0; page -1 outside the
+    // cache, -2 where the tile has no such key
+    auto look_up = [&](int key0, int& page, int& slot) {
+      const int pos = key0 + (lane << p.box_log2);
+      page = -2;
+      if (lane < boxes && pos < keys_all) {
+        const int blk = pos / a.block_size;
+        slot = pos - blk * a.block_size;
+        page = ldg_cg_i32(a.block_table + (long long)b * a.table_stride + blk);
+        if (page < 0 || page >= a.num_blocks) {
+          attn_error(a.status);
+          page = -1;
+        }
+      }
+    };
+    int page = -2, slot = 0, next_page = -2, next_slot = 0;
+    if (t0 < t1) look_up(t0 * kTile, page, slot);
+    for (int j = t0; j < t1; ++j, ++n_tile) {
+      if (j + 1 < t1) look_up((j + 1) * kTile, next_page, next_slot);
+      if (used && !wait(smem_addr(&C.empty[st]), ph ^ 1u, C, a.status)) {
+        ok = false;
+        break;
+      }
+      const uint32_t good = __ballot_sync(0xffffffffu, page >= 0), bad = __ballot_sync(0xffffffffu, page == -1);
+      if (kv == 0 && half == 0) {
+        TileInfo& info = C.info[n_tile % kInfo];
+        const int keys = min(kTile, keys_all - j * kTile);
+        if (bad) {
+          for (int w = 0; w < 4; ++w) {
+            const uint32_t x = __ballot_sync(0xffffffffu, (bad >> ((32 * w + lane) >> p.box_log2)) & 1u);
+            if (lane == 0) info.bad[w] = x;
+          }
+        }
+        if (lane == 0) {
+          info.keys = keys;
+          info.some_bad[0] = bad != 0;
+          info.some_bad[1] = 0;
+        }
+      }
+      if (lane == 0) bar_expect(smem_addr(&C.full[st]), (uint32_t)(__popc(good) * p.box * 128));
+      __syncwarp();
+      if (page >= 0)
+        tc::tma_load_4d(smem + kOffRing + st * kStageBytes + half * kHalf + (lane << p.box_log2) * 128, map, 64 * half,
+                        h, slot, page, &C.full[st]);
+      __syncwarp();
+      ++uses;
+      st += 2;
+      if (st >= (uint32_t)kStages) {
+        st -= (uint32_t)kStages;
+        used = true;
+        ph ^= 1u;
+      }
+      page = next_page;
+      slot = next_slot;
+    }
+  }
+  if (aborted(C)) {  // no copy may land after the block has exited
+    for (uint32_t i = uses < 3u ? 0u : uses - 3u; i < uses; ++i) {
+      const uint32_t x = 2 * i + (uint32_t)kv, t = globaltimer_low();
+      while (!bar_test(smem_addr(&C.full[x % kStages]), (x / kStages) & 1u) && globaltimer_low() - t < kWaitNs) {
+      }
+    }
   }
 }
 
@@ -723,14 +884,10 @@ FLINT_DEV void q_role(const Args& p, Ctl& C, uint8_t* smem, int t) {
 // sequence's end, or on a page outside the cache) is filled with zeros.  A
 // tile is handed over once the next one's copies are under way, or before
 // this warp has to wait.
-// PAGES16: pages of a multiple of 16 slots, so 16 keys from a multiple of 16
-// on lie at one stride; otherwise each key's place is looked up.
-template <bool PAGES16>
 FLINT_DEV void load_role(const Args& p, Ctl& C, uint8_t* smem, int kv, int part) {
   const AttnArgs& a = p.a;
   const int lane = threadIdx.x & 31, hi = lane >> 4, ch = lane & 15;
-  volatile int* abort = &C.abort;
-  const uint16_t* base = (kv ? a.v : a.k) + 8 * ch + (PAGES16 ? hi * a.s_slot : 0);
+  const uint16_t* base = (kv ? a.v : a.k) + 8 * ch;
   // where this lane's piece of key 2 i + hi goes, by i % 4
   uint32_t to[4];
 #pragma unroll
@@ -743,7 +900,7 @@ FLINT_DEV void load_role(const Args& p, Ctl& C, uint8_t* smem, int kv, int part)
   auto hand_over = [&]() {
     fence_proxy_async_smem();
     __syncwarp();
-    if (lane == 0) mbar_arrive(&C.full[pending]);
+    if (lane == 0) bar_arrive(smem_addr(&C.full[pending]));
   };
   auto flush = [&]() {
     if (pending >= 0) {
@@ -752,15 +909,14 @@ FLINT_DEV void load_role(const Args& p, Ctl& C, uint8_t* smem, int kv, int part)
       pending = -1;
     }
   };
-  // Offsets, -1 where there is none.  PAGES16: of the 16 keys from 16 (lane %
-  // 4) on; otherwise of keys lane and lane + 32 (of this warp's 64)
+  // offsets of keys lane and lane + 32 (of this warp's 64), -1 where there is none
   auto look_up = [&](const Piece& u, int key0, long long (&off)[2]) {
-    const int pos = key0 + 64 * part + (PAGES16 ? 16 * (lane & 3) : lane);
+    const int pos = key0 + 64 * part + lane;
     off[0] = pos < u.keys ? key_offset(a, u.b, pos) : -1;
-    if (!PAGES16) off[1] = pos + 32 < u.keys ? key_offset(a, u.b, pos + 32) : -1;
+    off[1] = pos + 32 < u.keys ? key_offset(a, u.b, pos + 32) : -1;
   };
   for (uint32_t n = 0;; ++n) {
-    if (!__all_sync(0xffffffffu, mbar_test_wait(&C.piece_full[n % kPieces], (n / kPieces) & 1))) flush();
+    if (!is_over(smem_addr(&C.piece_full[n % kPieces]), (n / kPieces) & 1)) flush();
     if (!piece_ready(C, n, a.status)) break;
     const Piece u = C.piece[n % kPieces];
     piece_done(C, n);
@@ -771,20 +927,13 @@ FLINT_DEV void load_role(const Args& p, Ctl& C, uint8_t* smem, int kv, int part)
       long long next[2] = {-1, -1};
       if (j + 1 < u.t1) look_up(u, (j + 1) * kTile, next);
       if (used) {
-        if (!__all_sync(0xffffffffu, mbar_test_wait(&C.empty[st], ph ^ 1u))) flush();
-        if (!wait(&C.empty[st], ph ^ 1u, abort, a.status)) break;
+        if (!is_over(smem_addr(&C.empty[st]), ph ^ 1u)) flush();
+        if (!wait(smem_addr(&C.empty[st]), ph ^ 1u, C, a.status)) break;
       }
       const int keys = u.keys - j * kTile - 64 * part;  // of this warp's 64 (may be more, or none)
       if (kv == 0) {
-        uint32_t b0, b1;
-        if (PAGES16) {
-          const uint32_t b = __ballot_sync(0xffffffffu, off[0] < 0 && 16 * (lane & 3) < keys);
-          b0 = (b & 1u ? 0xffffu : 0u) | (b & 2u ? 0xffff0000u : 0u);
-          b1 = (b & 4u ? 0xffffu : 0u) | (b & 8u ? 0xffff0000u : 0u);
-        } else {
-          b0 = __ballot_sync(0xffffffffu, off[0] < 0 && lane < keys);
-          b1 = __ballot_sync(0xffffffffu, off[1] < 0 && lane + 32 < keys);
-        }
+        const uint32_t b0 = __ballot_sync(0xffffffffu, off[0] < 0 && lane < keys);
+        const uint32_t b1 = __ballot_sync(0xffffffffu, off[1] < 0 && lane + 32 < keys);
         if (lane == 0) {
           TileInfo& info = C.info[n_tile % kInfo];
           info.some_bad[part] = (b0 | b1) != 0;
@@ -794,27 +943,13 @@ FLINT_DEV void load_role(const Args& p, Ctl& C, uint8_t* smem, int kv, int part)
         }
       }
       const uint32_t dst = smem_addr(smem + kOffRing + st * kStageBytes);
-      if (PAGES16) {
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          const long long o = __shfl_sync(0xffffffffu, off[0], x);
-          const uint16_t* from = src + (o < 0 ? 0 : o);
-          const int left = o < 0 ? 0 : keys - 16 * x - hi;  // keys from this lane's first on
+      for (int x = 0; x < 2; ++x)
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            cp_async16_or_zero(dst + (uint32_t)((8 * x + i) * 256) + to[i & 3], left > 2 * i ? from : src, left > 2 * i);
-            from += 2 * a.s_slot;
-          }
+        for (int i = 0; i < 16; ++i) {
+          const long long o = __shfl_sync(0xffffffffu, off[x], 2 * i + hi);
+          cp_async16_or_zero(dst + (uint32_t)((16 * x + i) * 256) + to[i & 3], src + (o < 0 ? 0 : o), o >= 0);
         }
-      } else {
-#pragma unroll
-        for (int x = 0; x < 2; ++x)
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const long long o = __shfl_sync(0xffffffffu, off[x], 2 * i + hi);
-            cp_async16_or_zero(dst + (uint32_t)((16 * x + i) * 256) + to[i & 3], src + (o < 0 ? 0 : o), o >= 0);
-          }
-      }
       cp_async_commit();
       if (pending >= 0) {
         cp_async_wait_group<1>();
@@ -830,17 +965,20 @@ FLINT_DEV void load_role(const Args& p, Ctl& C, uint8_t* smem, int kv, int part)
       off[0] = next[0];
       off[1] = next[1];
     }
-    if (*abort) break;
+    if (aborted(C)) break;
   }
   flush();
   cp_async_wait_all();  // no copy may land after the block has exited
 }
 
+// TILED: pages that tiled copies take; otherwise (tiny pages, strides that no
+// tensor map has) 16-byte copies.
+template <bool TILED>
 __global__ void __launch_bounds__(kThreads, 1)
-    attn_prompt_kernel(const __grid_constant__ Args p) {
+    attn_prompt_kernel(const __grid_constant__ Args p, const __grid_constant__ Maps maps) {
   SpanGuard<kSpanAttnPrompt> span_guard;
   extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+  uint8_t* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);  // (stays a shared-memory pointer)
   Ctl& C = *reinterpret_cast<Ctl*>(smem + kOffCtl);
   const int warp = threadIdx.x >> 5;
   if (threadIdx.x == 0) {
@@ -874,21 +1012,21 @@ __global__ void __launch_bounds__(kThreads, 1)
   pdl_launch_dependents();
   if (warp < kWarpMma) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
-    softmax_role(p, C, tmem, warp >> 2);
+    softmax_role<TILED>(p, C, smem, tmem, warp >> 2);
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
     if (warp == kWarpMma)
       mma_role(p, C, smem, tmem);
     else if (warp == kWarpWalk)
       walk_role(p, C);
-    else if (warp < kWarpLoad)
-      q_role(p, C, smem, warp - kWarpQ);
-    else {
-      const int kv = (warp - kWarpLoad) & 1, part = (warp - kWarpLoad) >> 1;
-      if (p.a.block_size % 16 == 0)
-        load_role<true>(p, C, smem, kv, part);
+    else if (warp == kWarpQ)
+      q_role(p, C, smem);
+    else if (warp != kWarpIdle) {
+      const int i = warp == kWarpLoad + 4 ? 3 : warp - kWarpLoad, kv = i & 1, part = i >> 1;
+      if (TILED)
+        load_tiled_role(p, maps, C, smem, kv, part);
       else
-        load_role<false>(p, C, smem, kv, part);
+        load_role(p, C, smem, kv, part);
     }
   }
   tc::fence_before_sync();
@@ -900,6 +1038,54 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // --------------------------------------------------------------- host side
+PFN_cuTensorMapEncodeTiled_v12000 encoder() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) != cudaSuccess)
+      f = nullptr;
+    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+  }();
+  return fn;
+}
+
+bool make_map(CUtensorMap* m, const AttnArgs& a, const uint16_t* base, int box) {
+  auto fn = encoder();
+  if (!fn) return false;
+  const cuuint64_t dims[4] = {kHeadDim, (cuuint64_t)a.nkv, (cuuint64_t)a.block_size, (cuuint64_t)a.num_blocks};
+  // the stride of an extent of 1 is never used, but has to be a valid one
+  const cuuint64_t strides[3] = {(cuuint64_t)(a.nkv > 1 ? a.s_head * 2 : 256),
+                                 (cuuint64_t)(a.block_size > 1 ? a.s_slot * 2 : 256),
+                                 (cuuint64_t)(a.num_blocks > 1 ? a.s_block * 2 : 256)};
+  for (cuuint64_t s : strides)
+    if (s == 0 || s >= (1ull << 40)) return false;
+  const cuuint32_t bx[4] = {64, 1, (cuuint32_t)box, 1};
+  const cuuint32_t es[4] = {1, 1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<uint16_t*>(base), dims, strides, bx, es,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <bool TILED>
+cudaError_t launch_main(const Args& p, const Maps& maps, int ctas, cudaLaunchConfig_t cfg) {
+  const void* fn = reinterpret_cast<const void*>(attn_prompt_kernel<TILED>);
+  static std::atomic<bool> allowed[64], checked;
+  cudaError_t err = allow_smem(fn, (int)kSmem, allowed);
+  if (err != cudaSuccess) return err;
+  if (!checked.load(std::memory_order_relaxed)) {
+    cudaFuncAttributes fa;
+    err = cudaFuncGetAttributes(&fa, fn);
+    if (err != cudaSuccess) return err;
+    if (fa.numRegs != kRegsLaunch) return cudaErrorInvalidConfiguration;  // the register split needs them
+    checked.store(true, std::memory_order_relaxed);
+  }
+  cfg.gridDim = dim3((unsigned)ctas);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmem;
+  void* args[] = {const_cast<Args*>(&p), const_cast<Maps*>(&maps)};
+  return cudaLaunchKernelExC(&cfg, fn, args);
+}
+
 }  // namespace
 
 PromptWs prompt_ws(void* base, int T, int B, int nq, int nkv) {
@@ -927,21 +1113,18 @@ cudaError_t launch_attn_prompt(const AttnArgs& a, const PromptWs& w, cudaStream_
   Args p;
   p.a = a;
   p.w = w;
+  p.box = 1;
+  p.box_log2 = 0;
+  while (p.box < kTile && a.block_size % (2 * p.box) == 0) {
+    p.box *= 2;
+    ++p.box_log2;
+  }
+  Maps maps = {};
+  const bool tiled = p.box >= kMinBox && make_map(&maps.k, a, a.k, p.box) && make_map(&maps.v, a, a.v, p.box);
   int sms = 0;
   cudaError_t err = device_sms(&sms);
   if (err != cudaSuccess) return err;
   int ctas = sms < kPromptCtas ? sms : kPromptCtas;
-  const void* fn = reinterpret_cast<const void*>(attn_prompt_kernel);
-  static std::atomic<bool> allowed[64], checked;
-  err = allow_smem(fn, (int)kSmem, allowed);
-  if (err != cudaSuccess) return err;
-  if (!checked.load(std::memory_order_relaxed)) {
-    cudaFuncAttributes fa;
-    err = cudaFuncGetAttributes(&fa, fn);
-    if (err != cudaSuccess) return err;
-    if (fa.numRegs != kRegsLaunch) return cudaErrorInvalidConfiguration;  // the register split needs them
-    checked.store(true, std::memory_order_relaxed);
-  }
   cudaLaunchConfig_t cfg = {};
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
@@ -954,11 +1137,7 @@ cudaError_t launch_attn_prompt(const AttnArgs& a, const PromptWs& w, cudaStream_
   void* plan_args[] = {&p, &ctas};
   err = cudaLaunchKernelExC(&cfg, reinterpret_cast<const void*>(attn_plan_kernel), plan_args);
   if (err != cudaSuccess) return err;
-  cfg.gridDim = dim3((unsigned)ctas);
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = kSmem;
-  void* args[] = {&p};
-  return cudaLaunchKernelExC(&cfg, fn, args);
+  return tiled ? launch_main<true>(p, maps, ctas, cfg) : launch_main<false>(p, maps, ctas, cfg);
 }
 
 FLINT_SPAN_SETTER(attn_prompt)

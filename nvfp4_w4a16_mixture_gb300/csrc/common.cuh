@@ -283,6 +283,12 @@ FLINT_DEV unsigned long long globaltimer_ns() {
   asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
   return t;
 }
+// Its low word (wraps after 4.3 s).
+FLINT_DEV uint32_t globaltimer_low() {
+  uint32_t t;
+  asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(t));
+  return t;
+}
 }  // namespace flint
 
 namespace flint {

@@ -256,6 +256,15 @@ FLINT_DEV void tma_load_2d(void* dst, const void* tmap, int c0, int c1, uint64_t
       : "memory");
 }
 
+// 4-D tiled load, as above.
+FLINT_DEV void tma_load_4d(void* dst, const void* tmap, int c0, int c1, int c2, int c3, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, "
+      "%3, %4, %5}], [%6];" ::"r"(smem_addr(dst)),
+      "l"(tmap), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(smem_addr(bar))
+      : "memory");
+}
+
 // Byte offset of element (r, k) (bf16, k < 64) inside a K-major 128-byte
 // swizzled tile.
 FLINT_DEV uint32_t sw128_offset(int r, int k) {
