@@ -71,8 +71,10 @@ static_assert(2 * kRegsSoftmax + 2 * kRegsOther <= 4 * kRegsLaunch, "setmaxnreg.
 constexpr int kInfo = 8;                   // key-tile records in flight
 constexpr int kPieces = 4;                 // pieces published ahead
 constexpr int kPieceReaders = 14;          // 8 softmax warps, MMA, Q, 4 loading ones
-constexpr int kUnitWeight = 3;             // a unit's fixed part, in tile products
-constexpr int kMinWeight = 8;              // least work of a CTA
+// Weights, in halves of a key tile's time (0.8 us): a unit's fixed part (Q,
+// first scores, output: about 5.5 us), and the least work worth a CTA of its
+// own (a unit below it is not cut: joining its parts would cost 3 us and more).
+constexpr int kTileWeight = 2, kUnitWeight = 7, kLeastWeight = 24;
 constexpr float kLazy = 8.0f;
 constexpr uint32_t kWaitNs = 200u * 1000 * 1000;
 constexpr uint32_t kSuspendNs = 50000;
@@ -164,20 +166,21 @@ constexpr int kMinBox = 4;  // smallest box worth a tiled copy: 32 per key tile 
 
 // ---------------------------------------------------------------- the plan
 // A CTA's start record: {entry, kv head, offset in the unit, CTAs at work},
-// {total weight, the piece's weight} as 64-bit values, the entry.
-constexpr int kStartWords = 4;
+// {total weight, the piece's weight} as 64-bit values, the entry, {least}.
+constexpr int kStartWords = 5;
 // Entry: up to 256 packed rows of a sequence (all kv heads).
 struct Entry {
   int b, lo, n, keys;     // sequence, its first q row, its q rows, its keys
-  int r0, rows, tiles, mul;  // packed rows, key tiles seen, row tiles at work
+  int r0, rows, tiles, unused;  // packed rows, key tiles seen
 };
-FLINT_DEV long long weight(const Entry& e) { return (long long)e.tiles * e.mul + kUnitWeight; }
+// least: 0, or what each unit weighs at least (little work in all)
+FLINT_DEV int weight(const Entry& e, int least) { return max(e.tiles * kTileWeight + kUnitWeight, least); }
 
 FLINT_DEV Entry load_entry(const int4* p) {
   const uint4 x = ldg_cg_v4(p), y = ldg_cg_v4(p + 1);
   Entry e;
   e.b = (int)x.x; e.lo = (int)x.y; e.n = (int)x.z; e.keys = (int)x.w;
-  e.r0 = (int)y.x; e.rows = (int)y.y; e.tiles = (int)y.z; e.mul = (int)y.w;
+  e.r0 = (int)y.x; e.rows = (int)y.y; e.tiles = (int)y.z; e.unused = 0;
   return e;
 }
 
@@ -247,25 +250,32 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const Args p, i
       const int seen = max(0, min(keys, keys - n + (r0 + rows - 1) / G + 1));  // by its last row
       p.w.entries[2 * (long long)e] = make_int4(b, lo, n, keys);
       p.w.entries[2 * (long long)e + 1] =
-          make_int4(r0, rows, (seen + kTile - 1) / kTile, rows > kTile ? 2 : 1);
+          make_int4(r0, rows, (seen + kTile - 1) / kTile, 0);
     }
   }
   __syncthreads();
   long long total = 0;
-  for (long long e0 = 0; e0 < n_entries; e0 += kPlanThreads) {
-    const long long e = e0 + tid;
-    long long all;
-    const long long at = total + scan_cta64(e < n_entries ? weight(load_entry(p.w.entries + 2 * e)) * a.nkv : 0, warps, &all);
-    if (e < n_entries) p.w.prefix[e] = at;
-    total += all;
+  int least = 0;
+  for (;;) {
+    total = 0;
+    for (long long e0 = 0; e0 < n_entries; e0 += kPlanThreads) {
+      const long long e = e0 + tid;
+      long long all;
+      const long long mine = e < n_entries ? (long long)weight(load_entry(p.w.entries + 2 * e), least) * a.nkv : 0;
+      const long long at = total + scan_cta64(mine, warps, &all);
+      if (e < n_entries) p.w.prefix[e] = at;
+      total += all;
+    }
+    if (least != 0 || total / ctas >= kLeastWeight) break;
+    least = kLeastWeight;
   }
   if (tid == 0) p.w.prefix[n_entries] = total;
   __syncthreads();
-  const long long n_cta = total == 0 ? 0 : max(1ll, min((long long)ctas, total / kMinWeight));
+  const long long n_cta = total == 0 ? 0 : max(1ll, min((long long)ctas, total / kLeastWeight));
   if (tid < ctas && tid >= n_cta) p.w.starts[kStartWords * tid] = make_int4(0, 0, 0, 0);
   // CTA c's piece begins at floor(c total / n_cta); entry e writes those inside it
   for (long long e = tid; e < n_entries; e += kPlanThreads) {
-    const long long w = weight(load_entry(p.w.entries + 2 * e)), at = p.w.prefix[e], end = at + w * a.nkv;
+    const long long w = weight(load_entry(p.w.entries + 2 * e), least), at = p.w.prefix[e], end = at + w * a.nkv;
     for (long long c = (at * n_cta + total - 1) / total; c < n_cta; ++c) {
       const long long pos = c * total / n_cta;
       if (pos >= end) break;
@@ -275,6 +285,7 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const Args p, i
       s[1] = make_int4((int)total, (int)(total >> 32), (int)rem, (int)(rem >> 32));
       s[2] = p.w.entries[2 * e];
       s[3] = p.w.entries[2 * e + 1];
+      s[4] = make_int4(least, 0, 0, 0);
     }
   }
 }
@@ -286,6 +297,7 @@ FLINT_DEV void walk_role(const Args& p, Ctl& C) {
   const int lane = threadIdx.x & 31, cta = blockIdx.x, nkv = p.a.nkv;
   const int4* start = p.w.starts + kStartWords * cta;
   const uint4 s0 = ldg_cg_v4(start), s1 = ldg_cg_v4(start + 1);
+  const int least = ldg_cg_i32(reinterpret_cast<const int*>(start + 4));
   Entry e = load_entry(start + 2);
   int i = (int)s0.x, h = (int)s0.y, off = (int)s0.z;
   const long long ctas = (int)s0.w, total = (long long)((unsigned long long)s1.y << 32 | s1.x);
@@ -304,14 +316,14 @@ FLINT_DEV void walk_role(const Args& p, Ctl& C) {
   };
   Piece x;
   while (rem > 0) {
-    const int w = (int)weight(e);
+    const int w = weight(e, least);
     const int take = (int)min((long long)(w - off), rem);
-    const int real = max(1, e.tiles * e.mul);
+    const int real = max(1, e.tiles * kTileWeight);
     if (off < real) {
       x.b = e.b; x.lo = e.lo; x.n = e.n; x.keys = e.keys;
       x.r0 = e.r0; x.rows = e.rows; x.h = h;
-      x.t0 = min(off / e.mul, e.tiles);
-      x.t1 = min((off + take) / e.mul, e.tiles);
+      x.t0 = min(off / kTileWeight, e.tiles);
+      x.t1 = min((off + take) / kTileWeight, e.tiles);
       x.c_first = x.c_last = cta;
       x.valid = 1;
       if (off > 0 || take < real) {  // CTA of position y: floor(((y + 1) ctas - 1) / total)
