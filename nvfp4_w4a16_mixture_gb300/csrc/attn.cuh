@@ -32,20 +32,6 @@ FLINT_DEV int seq_keys(const AttnArgs& a, int b) {
   return n;
 }
 
-// Rows [lo, lo + n) of q that sequence b owns (decode: row b).
-FLINT_DEV void seq_rows(const AttnArgs& a, int b, int& lo, int& n) {
-  if (!a.cu_q) {
-    lo = b;
-    n = 1;
-    return;
-  }
-  const int c0 = ldg_cg_i32(a.cu_q + b), c1 = ldg_cg_i32(a.cu_q + b + 1);
-  lo = c0;
-  n = min(c1, a.T) - c0;
-  if (c0 < 0 || c1 < c0 || c1 > a.T) attn_error(a.status);
-  if (c0 < 0 || n < 0) n = 0;
-}
-
 // Element offset of the key at position pos of sequence b, head 0, or -1 for
 // a page outside the cache.
 FLINT_DEV long long key_offset(const AttnArgs& a, int b, int pos) {

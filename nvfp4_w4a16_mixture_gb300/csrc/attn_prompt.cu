@@ -165,6 +165,15 @@ struct Maps {
 constexpr int kMinBox = 4;  // smallest box worth a tiled copy: 32 per key tile and half
 
 // ---------------------------------------------------------------- the plan
+// Rows [lo, lo + n) of q that sequence b owns.
+FLINT_DEV void seq_rows(const AttnArgs& a, int b, int& lo, int& n) {
+  const int c0 = ldg_cg_i32(a.cu_q + b), c1 = ldg_cg_i32(a.cu_q + b + 1);
+  lo = c0;
+  n = min(c1, a.T) - c0;
+  if (c0 < 0 || c1 < c0 || c1 > a.T) attn_error(a.status);
+  if (c0 < 0 || n < 0) n = 0;
+}
+
 // A CTA's start record: {entry, kv head, offset in the unit, CTAs at work},
 // {total weight, the piece's weight} as 64-bit values, the entry, {least}.
 constexpr int kStartWords = 5;

@@ -1,16 +1,14 @@
-// Attention of few query rows over the paged cache: one new token per
-// sequence (flint_attn_decode), and prompts whose cache cannot be read by
-// tiled copies.
+// Attention of one new token per sequence over the paged cache
+// (flint_attn_decode).
 //
-// The rows of one sequence and kv head are its tokens' query heads packed
-// together: packed row r is token r / G, head r % G of the group (G query
+// The rows of one sequence and kv head are the query heads of its group (G
 // heads per kv head), so one pass over the keys serves the whole group.  A
-// unit is 8 NT packed rows of one (sequence, kv head) and all its keys, in
+// unit is up to 8 NT rows of one (sequence, kv head) and all its keys, in
 // tiles of 128: 16 keys for each of the CTA's 8 warps.
 //
 // Per 16 keys a warp forms S^T = K Q^T and O^T += V^T P on mma.sync
 // m16n8k16 with the keys (then the head's dims) as the 16-row operand and 8
-// packed rows as the 8 columns, so a group of 8 heads wastes nothing.  The
+// rows as the 8 columns, so a group of 8 heads wastes nothing.  The
 // bytes that a lane's operand registers need are the lane's own 16-byte
 // pieces of the cache:
 //  - K: lane (g, t) = (lane / 4, lane % 4) takes dims 32 i + 8 t .. + 7 of
@@ -46,7 +44,7 @@ namespace {
 constexpr int kRowsWarps = 8;
 constexpr int kRowsThreads = kRowsWarps * 32;
 constexpr int kTileKeys = 16 * kRowsWarps;
-constexpr int kUnitWeight = 1;  // a unit's fixed part, in tiles
+constexpr int kUnitWeight = 2;  // a unit's fixed part, in tiles (2.3 us beside 1 us for a tile of 64 KB)
 constexpr int kMinWeight = 1;   // least work of a CTA
 constexpr int kChunkBytes = 16 * kHeadDim * 2 * 2;  // 16 keys' K and V
 constexpr float kLazy = 8.0f;
@@ -67,12 +65,11 @@ FLINT_DEV uint32_t pack_bf16(float a, float b) {
   return *reinterpret_cast<uint32_t*>(&r);
 }
 
-// One part of a unit: rows r0 .. of sequence b's packed rows, kv head h, key
+// One part of a unit: rows r0 .. of the group of kv head h, sequence b, key
 // tiles [t0, t1).
 struct Part {
   int b, h, r0, rows;
-  int lo, n, keys;      // the sequence's first q row, its q rows, its keys
-  int seen;             // keys up to the last row's last
+  int keys;             // of the sequence
   int t0, t1;
   int c_first, c_last;  // CTAs that share the unit
 };
@@ -83,13 +80,11 @@ struct Walk {
   long long total, ctas, rem;
   long long at;  // position of the sequence's first unit
   int b, unit, off;
-  int lo, n, keys, tiles, units;
+  int keys, tiles, units;  // of the sequence; units is the same for all
 
   FLINT_DEV void sequence(const AttnArgs& a) {
-    seq_rows(a, b, lo, n);
     keys = seq_keys(a, b);
     tiles = (keys + kTileKeys - 1) / kTileKeys;
-    units = (n * (a.nq / a.nkv) + 8 * NT - 1) / (8 * NT) * a.nkv;
   }
   FLINT_DEV bool next(const AttnArgs& a, Part& p) {
     while (rem > 0) {
@@ -109,11 +104,8 @@ struct Walk {
         p.b = b;
         p.h = unit % a.nkv;
         p.r0 = unit / a.nkv * 8 * NT;
-        p.rows = min(8 * NT, n * G - p.r0);
-        p.lo = lo;
-        p.n = n;
+        p.rows = min(8 * NT, G - p.r0);
         p.keys = keys;
-        p.seen = max(0, min(keys, keys - n + (p.r0 + p.rows - 1) / G + 1));
         p.t0 = min(off, tiles);
         p.t1 = min(off + take, tiles);
         p.c_first = p.c_last = blockIdx.x;
@@ -137,16 +129,12 @@ struct Walk {
 
 template <int NT>
 struct Acc {
-  float o[NT][8][4];  // tile j: {dim 8g+j, 64+8g+j} x packed rows 2t, 2t+1 of 8-row tile nt
+  float o[NT][8][4];  // tile j: {dim 8g+j, 64+8g+j} x rows 2t, 2t+1 of 8-row tile nt
   float m[NT][2], l[NT][2];
 };
 
-// Token (within the sequence's rows) and query head of packed row r.
-FLINT_DEV void row_of(const AttnArgs& a, const Part& u, int r, int& token, int& head) {
-  const int G = a.nq / a.nkv, R = u.r0 + r;
-  token = R / G;
-  head = u.h * G + R % G;
-}
+// Query head of row r of the part.
+FLINT_DEV int head_of(const AttnArgs& a, const Part& u, int r) { return u.h * (a.nq / a.nkv) + u.r0 + r; }
 
 // The warps' parts of 8 NT rows, joined in warp order.
 template <int NT>
@@ -200,15 +188,13 @@ FLINT_DEV float part_factor(float pm, float pl, float m) {
 // Four dims of a finished row: o / l in bf16 (zeros where no key had any
 // weight), and its lse.
 FLINT_DEV void write_row(const AttnArgs& a, const Part& u, int r, int d4, float4 o, float m, float l) {
-  int token, head;
-  row_of(a, u, r, token, head);
+  const long long row = (long long)u.b * a.nq + head_of(a, u, r);
   const float inv = l == 0.0f ? 0.0f : 1.0f / l;
   uint2 w;
   w.x = pack_bf16(o.x * inv, o.y * inv);
   w.y = pack_bf16(o.z * inv, o.w * inv);
-  const long long row = u.lo + token;
-  *reinterpret_cast<uint2*>(a.out + (row * a.nq + head) * kHeadDim + 4 * d4) = w;
-  if (a.lse && d4 == 0) a.lse[row * a.nq + head] = l == 0.0f ? neg_inf() : (m + log2f(l)) * 0.6931471805599453f;
+  *reinterpret_cast<uint2*>(a.out + row * kHeadDim + 4 * d4) = w;
+  if (a.lse && d4 == 0) a.lse[row] = l == 0.0f ? neg_inf() : (m + log2f(l)) * 0.6931471805599453f;
 }
 
 // This CTA's piece of the line: [pos, end) of total, and the unit it starts in.
@@ -218,18 +204,16 @@ FLINT_DEV bool find_piece(const AttnArgs& a, Parts<NT>& P, Walk<NT>& k) {
   // two rounds over the sequences: the total, then the start (one round where
   // all sequences fit the CTA's threads)
   long long total = 0, pos = -1, end = 0;
+  k.units = (a.nq / a.nkv + 8 * NT - 1) / (8 * NT) * a.nkv;
   for (int round = 0; round < 2; ++round) {
     long long base = 0;
     for (int b0 = 0; b0 < a.B; b0 += kRowsThreads) {
       const int b = b0 + tid;
       long long w = 0;
-      int tiles = 0, units = 0;
+      int tiles = 0;
       if (b < a.B) {
-        int lo, n;
-        seq_rows(a, b, lo, n);
         tiles = (seq_keys(a, b) + kTileKeys - 1) / kTileKeys;
-        units = (n * (a.nq / a.nkv) + 8 * NT - 1) / (8 * NT) * a.nkv;
-        w = (long long)units * (tiles + kUnitWeight);
+        w = (long long)k.units * (tiles + kUnitWeight);
       }
       long long x = w;
 #pragma unroll
@@ -275,7 +259,9 @@ FLINT_DEV bool find_piece(const AttnArgs& a, Parts<NT>& P, Walk<NT>& k) {
   return true;
 }
 
-template <int NT>
+// GS: keys that lie at one stride (4 where pages have a multiple of 4 slots,
+// else 1), so a look-up of the page table by all lanes serves 2 * GS chunks.
+template <int NT, int GS>
 __global__ void __launch_bounds__(kRowsThreads, 1) attn_rows_kernel(const __grid_constant__ Args args) {
   SpanGuard<kSpanAttnRows> span_guard;
   pdl_wait();  // q and the cache's newest rows are the previous kernel's output
@@ -290,78 +276,95 @@ __global__ void __launch_bounds__(kRowsThreads, 1) attn_rows_kernel(const __grid
   if (!find_piece(a, P, comp)) return;
 
   // ---- the fetch side: a walk of its own, ahead of the products
+  constexpr int kPer = 16 / GS, kChunks = 32 / kPer;  // look-ups per chunk, chunks per look-up
   Walk<NT> fwalk = comp;
-  Part f;
-  int ftile = 0;       // next tile to fetch
-  long long foff = -1; // element offset of key lane % 16 of that chunk, or -1
+  Part f = {};
+  int ftile = 0, fpos = 0;    // next tile to fetch, its place in the look-up
+  long long cur = -1, nxt = -1;  // element offsets of GS keys each, -1: none
+  uint32_t cur_ok = 0;        // which of them are there
   bool fmore = true;
   auto chunk_key = [&](int tile) { return tile * kTileKeys + 16 * warp; };
-  auto look_up = [&]() {  // the pages of chunk (f, ftile)
-    const int key = chunk_key(ftile) + (lane & 15);
-    foff = key < f.seen ? key_offset(a, f.b, key) : -1;
+  auto look_up = [&](int tile) {
+    const int at = tile + lane / kPer, key = chunk_key(at) + lane % kPer * GS;
+    return at < f.t1 && key < f.keys ? key_offset(a, f.b, key) : -1ll;
   };
   auto to_chunk = [&]() {  // on to this warp's next chunk, over the units
-    while (fmore && (ftile >= f.t1 || chunk_key(ftile) >= f.seen)) {
-      fmore = fwalk.next(a, f);
-      ftile = f.t0;
+    if (ftile < f.t1 && chunk_key(ftile) < f.keys) {
+      if (++fpos < kChunks) return;
+      cur = nxt;
+      nxt = look_up(ftile + kChunks);
+    } else {
+      do {
+        fmore = fwalk.next(a, f);
+        ftile = f.t0;
+      } while (fmore && (ftile >= f.t1 || chunk_key(ftile) >= f.keys));
+      if (!fmore) return;
+      cur = look_up(ftile);
+      nxt = look_up(ftile + kChunks);
     }
-    if (fmore) look_up();
+    fpos = 0;
+    cur_ok = __ballot_sync(0xffffffffu, cur >= 0);
   };
   uint4* ring = reinterpret_cast<uint4*>(smem) + (size_t)warp * kDepth<NT> * (kChunkBytes / 16) + lane;
-  auto fetch = [&](int slot) -> uint32_t {  // fills a slot; the mask of its valid keys
-    uint32_t valid = 0;
+  auto fetch = [&](int slot) -> uint32_t {  // fills a slot; which of its GS-key groups are there
+    uint32_t there = 0;
     if (fmore) {
       const uint32_t dst = smem_addr(ring + slot * (kChunkBytes / 16));
-      valid = __ballot_sync(0xffffffffu, foff >= 0);
+      const int left = f.keys - chunk_key(ftile), l0 = fpos * kPer;  // keys from the chunk's first on
+      there = (cur_ok >> l0) & ((1u << kPer) - 1u);
       const uint16_t* kb = a.k + (long long)f.h * a.s_head + 8 * t;
       const uint16_t* vb = a.v + (long long)f.h * a.s_head + 8 * g;
+      auto place = [&](int key, long long o) { return o + (GS > 1 ? (long long)(key % GS) * a.s_slot : 0ll); };
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const long long o = __shfl_sync(0xffffffffu, foff, g + 8 * e);
-        const uint16_t* src = kb + (o < 0 ? 0 : o);
+        const int key = g + 8 * e;
+        const long long o = __shfl_sync(0xffffffffu, cur, l0 + key / GS);
+        const bool ok = o >= 0 && key < left;
+        const uint16_t* src = kb + (ok ? place(key, o) : 0ll);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) cp_async16_or_zero(dst + 512 * (4 * e + i), src + 32 * i, o >= 0);
+        for (int i = 0; i < 4; ++i) cp_async16_or_zero(dst + 512 * (4 * e + i), src + 32 * i, ok);
       }
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const long long o = __shfl_sync(0xffffffffu, foff, 2 * t + (e & 1) + 8 * (e >> 1));
-        const uint16_t* src = vb + (o < 0 ? 0 : o);
+      for (int e = 0; e < 2; ++e) {
+        const int key = 2 * t + 8 * e;
+        const long long o0 = __shfl_sync(0xffffffffu, cur, l0 + key / GS);
+        const long long o1 = GS > 1 ? o0 : __shfl_sync(0xffffffffu, cur, l0 + key + 1);
 #pragma unroll
-        for (int i = 0; i < 2; ++i) cp_async16_or_zero(dst + 512 * (8 + 2 * e + i), src + 64 * i, o >= 0);
+        for (int d = 0; d < 2; ++d) {
+          const long long o = d ? o1 : o0;
+          const bool ok = o >= 0 && key + d < left;
+          const uint16_t* src = vb + (ok ? place(key + d, o) : 0ll);
+#pragma unroll
+          for (int i = 0; i < 2; ++i) cp_async16_or_zero(dst + 512 * (8 + 2 * (2 * e + d) + i), src + 64 * i, ok);
+        }
       }
       ++ftile;
       to_chunk();
     }
     cp_async_commit();
-    return valid;
+    return there;
   };
-  f.t1 = 0;
-  ftile = 0;
-  f.seen = 0;
   to_chunk();
-  uint32_t valid[kDepth<NT>];
+  uint32_t there[kDepth<NT>];
 #pragma unroll
-  for (int i = 0; i < kDepth<NT>; ++i) valid[i] = fetch(i);
+  for (int i = 0; i < kDepth<NT>; ++i) there[i] = fetch(i);
   int slot = 0;
 
   Part u;
   while (comp.next(a, u)) {
-    // ---- Q of the unit's rows, and the last key that each sees
+    if (u.t0 >= u.t1) {  // a sequence without keys
+      for (int i = threadIdx.x; i < u.rows * 32; i += kRowsThreads)
+        write_row(a, u, i >> 5, i & 31, make_float4(0.0f, 0.0f, 0.0f, 0.0f), 0.0f, 0.0f);
+      continue;
+    }
+    // ---- Q of the unit's rows
     uint4 qf[NT][4];
-    int lim[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      int token, head;
-      row_of(a, u, 8 * nt + g, token, head);
       const bool ok = 8 * nt + g < u.rows;
-      const uint16_t* p = a.q + (long long)(u.lo + token) * a.q_stride + (long long)head * kHeadDim + 8 * t;
+      const uint16_t* p = a.q + (long long)u.b * a.q_stride + (long long)head_of(a, u, 8 * nt + g) * kHeadDim + 8 * t;
 #pragma unroll
       for (int i = 0; i < 4; ++i) qf[nt][i] = ok ? ldg_cg_v4(p + 32 * i) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        row_of(a, u, 8 * nt + 2 * t + e, token, head);
-        lim[nt][e] = u.keys - u.n + token;
-      }
     }
     Acc<NT> A;
 #pragma unroll
@@ -376,11 +379,11 @@ __global__ void __launch_bounds__(kRowsThreads, 1) attn_rows_kernel(const __grid
         A.l[nt][e] = 0.0f;
       }
     }
-    for (int tile = u.t0; tile < u.t1 && chunk_key(tile) < u.seen; ++tile) {
+    for (int tile = u.t0; tile < u.t1 && chunk_key(tile) < u.keys; ++tile) {
       const int key0 = chunk_key(tile);
       cp_async_wait_group<kDepth<NT> - 1>();
       const uint4* src = ring + slot * (kChunkBytes / 16);
-      const uint32_t ok = valid[0];
+      const uint32_t ok = there[0];
       float s[NT][4];
       {
         uint4 kr[2][4];
@@ -404,14 +407,14 @@ __global__ void __launch_bounds__(kRowsThreads, 1) attn_rows_kernel(const __grid
       for (int e = 0; e < 4; ++e)
 #pragma unroll
         for (int i = 0; i < 2; ++i) vr[e][i] = src[32 * (8 + 2 * e + i)];
-      // s[nt][2 e + i]: key g + 8 e, packed row 2t + i
+      // s[nt][2 e + i]: key g + 8 e, row 2t + i
       bool raise = false;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int kk = g + 8 * (i >> 1);
-          if (!((ok >> kk) & 1u) || key0 + kk > lim[nt][i & 1]) s[nt][i] = neg_inf();
+          if (!((ok >> (kk / GS)) & 1u) || key0 + kk >= u.keys) s[nt][i] = neg_inf();
           raise |= s[nt][i] * c > A.m[nt][i & 1] + kLazy;
         }
       if (__any_sync(0xffffffffu, raise)) {
@@ -470,8 +473,8 @@ __global__ void __launch_bounds__(kRowsThreads, 1) attn_rows_kernel(const __grid
       }
       // the slot's pieces are in registers: fill it again
 #pragma unroll
-      for (int i = 0; i + 1 < kDepth<NT>; ++i) valid[i] = valid[i + 1];
-      valid[kDepth<NT> - 1] = fetch(slot);
+      for (int i = 0; i + 1 < kDepth<NT>; ++i) there[i] = there[i + 1];
+      there[kDepth<NT> - 1] = fetch(slot);
       slot = slot + 1 == kDepth<NT> ? 0 : slot + 1;
     }
     // ---- the unit's end in this CTA
@@ -519,27 +522,40 @@ __global__ void __launch_bounds__(kRowsThreads, 1) attn_rows_kernel(const __grid
       }
       __syncthreads();
       if (P.last) {
-        for (int i = threadIdx.x; i < u.rows * 32; i += kRowsThreads) {
-          const int r = i >> 5, d4 = i & 31;
+        // a warp per row: the parts' references and sums one per lane, then
+        // their outputs, several loads under way
+        const int n = u.c_last - u.c_first + 1;
+        auto part_at = [&](int i) {
+          const int x = u.c_first + i;
+          return args.w.parts + (size_t)(2 * x + (i == 0)) * kPartFloats<NT>;
+        };
+        for (int r = warp; r < u.rows; r += kRowsWarps) {
           float m = neg_inf();
-#pragma unroll 8
-          for (int x = u.c_first; x <= u.c_last; ++x)
-            m = fmaxf(m, __ldcg(args.w.parts + (size_t)(2 * x + (x == u.c_first)) * kPartFloats<NT> + 8 * NT * kHeadDim + r));
+          for (int i = lane; i < n; i += 32) m = fmaxf(m, __ldcg(part_at(i) + 8 * NT * kHeadDim + r));
+#pragma unroll
+          for (int d = 16; d >= 1; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
           float l = 0.0f;
           float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+          for (int i0 = 0; i0 < n; i0 += 32) {
+            float y = 0.0f, yl = 0.0f;
+            if (i0 + lane < n) {
+              const float pl = __ldcg(part_at(i0 + lane) + 8 * NT * (kHeadDim + 1) + r);
+              y = part_factor(__ldcg(part_at(i0 + lane) + 8 * NT * kHeadDim + r), pl, m);
+              yl = y * pl;
+            }
+            const int here = min(32, n - i0);
 #pragma unroll 8
-          for (int x = u.c_first; x <= u.c_last; ++x) {
-            const float* pp = args.w.parts + (size_t)(2 * x + (x == u.c_first)) * kPartFloats<NT>;
-            const float pl = __ldcg(pp + 8 * NT * (kHeadDim + 1) + r);
-            const float y = part_factor(__ldcg(pp + 8 * NT * kHeadDim + r), pl, m);
-            const float4 v = __ldcg(reinterpret_cast<const float4*>(pp + r * kHeadDim + 4 * d4));
-            l += y * pl;
-            o.x += y * v.x;
-            o.y += y * v.y;
-            o.z += y * v.z;
-            o.w += y * v.w;
+            for (int i = 0; i < here; ++i) {
+              const float f = __shfl_sync(0xffffffffu, y, i);
+              l += __shfl_sync(0xffffffffu, yl, i);
+              const float4 v = __ldcg(reinterpret_cast<const float4*>(part_at(i0 + i) + r * kHeadDim + 4 * lane));
+              o.x += f * v.x;
+              o.y += f * v.y;
+              o.z += f * v.z;
+              o.w += f * v.w;
+            }
           }
-          write_row(a, u, r, d4, o, m, l);
+          write_row(a, u, r, lane, o, m, l);
         }
       }
     }
@@ -548,9 +564,9 @@ __global__ void __launch_bounds__(kRowsThreads, 1) attn_rows_kernel(const __grid
   cp_async_wait_all();
 }
 
-template <int NT>
+template <int NT, int GS>
 cudaError_t launch_nt(const AttnArgs& a, const RowsWs& w, cudaStream_t st) {
-  const void* fn = reinterpret_cast<const void*>(attn_rows_kernel<NT>);
+  const void* fn = reinterpret_cast<const void*>(attn_rows_kernel<NT, GS>);
   static std::atomic<bool> allowed[64];
   cudaError_t err = allow_smem(fn, (int)kSmem<NT>, allowed);
   if (err != cudaSuccess) return err;
@@ -587,10 +603,11 @@ RowsWs rows_ws(void* base) {
 }
 
 cudaError_t launch_attn_rows(const AttnArgs& a, const RowsWs& w, cudaStream_t st) {
-  // 8 packed rows per unit where a token's group fits them, else 16 (the keys
-  // are read once per unit)
-  const bool small = !a.cu_q && a.nq / a.nkv <= 8;
-  return small ? launch_nt<1>(a, w, st) : launch_nt<2>(a, w, st);
+  // 8 rows per unit where a group fits them, else 16 (the keys are read once
+  // per unit)
+  const bool small = a.nq / a.nkv <= 8;
+  if (a.block_size % 4 == 0) return small ? launch_nt<1, 4>(a, w, st) : launch_nt<2, 4>(a, w, st);
+  return small ? launch_nt<1, 1>(a, w, st) : launch_nt<2, 1>(a, w, st);
 }
 
 FLINT_SPAN_SETTER(attn_rows)
