@@ -44,7 +44,6 @@
 // hold).  Every wait is bounded (FLINT_ERR_TIMEOUT in the
 // status word on expiry).
 #include <cuda.h>
-#include <cudaTypedefs.h>
 
 #include "attn.cuh"
 #include "tc.cuh"
@@ -162,7 +161,6 @@ struct Args {
 struct Maps {
   CUtensorMap k, v;  // {128, heads, slots, pages}, box {64, 1, box, 1}
 };
-constexpr int kMinBox = 4;  // smallest box worth a tiled copy: 32 per key tile and half
 
 // ---------------------------------------------------------------- the plan
 // Rows [lo, lo + n) of q that sequence b owns.
@@ -1059,34 +1057,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // --------------------------------------------------------------- host side
-PFN_cuTensorMapEncodeTiled_v12000 encoder() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
-    void* f = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) != cudaSuccess)
-      f = nullptr;
-    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
-  }();
-  return fn;
-}
-
-bool make_map(CUtensorMap* m, const AttnArgs& a, const uint16_t* base, int box) {
-  auto fn = encoder();
-  if (!fn) return false;
-  const cuuint64_t dims[4] = {kHeadDim, (cuuint64_t)a.nkv, (cuuint64_t)a.block_size, (cuuint64_t)a.num_blocks};
-  // the stride of an extent of 1 is never used, but has to be a valid one
-  const cuuint64_t strides[3] = {(cuuint64_t)(a.nkv > 1 ? a.s_head * 2 : 256),
-                                 (cuuint64_t)(a.block_size > 1 ? a.s_slot * 2 : 256),
-                                 (cuuint64_t)(a.num_blocks > 1 ? a.s_block * 2 : 256)};
-  for (cuuint64_t s : strides)
-    if (s == 0 || s >= (1ull << 40)) return false;
-  const cuuint32_t bx[4] = {64, 1, (cuuint32_t)box, 1};
-  const cuuint32_t es[4] = {1, 1, 1, 1};
-  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<uint16_t*>(base), dims, strides, bx, es,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 template <bool TILED>
 cudaError_t launch_main(const Args& p, const Maps& maps, int ctas, cudaLaunchConfig_t cfg) {
   const void* fn = reinterpret_cast<const void*>(attn_prompt_kernel<TILED>);
@@ -1134,14 +1104,10 @@ cudaError_t launch_attn_prompt(const AttnArgs& a, const PromptWs& w, cudaStream_
   Args p;
   p.a = a;
   p.w = w;
-  p.box = 1;
-  p.box_log2 = 0;
-  while (p.box < kTile && a.block_size % (2 * p.box) == 0) {
-    p.box *= 2;
-    ++p.box_log2;
-  }
+  p.box = attn_box(a.block_size, kTile);
+  for (p.box_log2 = 0; (1 << p.box_log2) < p.box;) ++p.box_log2;
   Maps maps = {};
-  const bool tiled = p.box >= kMinBox && make_map(&maps.k, a, a.k, p.box) && make_map(&maps.v, a, a.v, p.box);
+  const bool tiled = p.box >= kAttnMinBox && attn_map(&maps.k, a, a.k, p.box) && attn_map(&maps.v, a, a.v, p.box);
   int sms = 0;
   cudaError_t err = device_sms(&sms);
   if (err != cudaSuccess) return err;

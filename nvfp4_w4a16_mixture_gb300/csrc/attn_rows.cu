@@ -6,22 +6,16 @@
 // unit is up to 8 NT rows of one (sequence, kv head) and all its keys, in
 // tiles of 128: 16 keys for each of the CTA's 8 warps.
 //
-// Per 16 keys a warp forms S^T = K Q^T and O^T += V^T P on mma.sync
+// Per 16 keys (a chunk) a warp forms S^T = K Q^T and O^T += V^T P on mma.sync
 // m16n8k16 with the keys (then the head's dims) as the 16-row operand and 8
-// rows as the 8 columns, so a group of 8 heads wastes nothing.  The
-// bytes that a lane's operand registers need are the lane's own 16-byte
-// pieces of the cache:
-//  - K: lane (g, t) = (lane / 4, lane % 4) takes dims 32 i + 8 t .. + 7 of
-//    keys g and g + 8; the four words are the operands of two k-steps (Q is
-//    loaded with the same permutation of the dims, and a sum does not depend
-//    on their order);
-//  - V: lane (g, t) takes dims 8 g .. + 7 and 64 + 8 g .. + 7 of keys 2t,
-//    2t + 1, 2t + 8, 2t + 9; a byte permutation pairs two keys' values of one
-//    dim, and dim 8 g + j (64 + 8 g + j) is row g (g + 8) of tile j.
-// So each lane copies its own pieces ahead of use (cp.async into a ring of
-// kDepth chunks of 8 KB per warp) and reads back only what it wrote: no
-// barrier in the loop, and the ring runs on across units.
-// P's accumulator layout (row = key) becomes the operand layout (row = packed
+// rows as the 8 columns, so a group of 8 heads wastes nothing.  Each warp has
+// a ring of its own, kDepth chunks of 8 KB in shared memory, that it fills
+// ahead of use (on across units) with tiled copies of a page's slots and
+// drains with ldmatrix (V transposed); no barrier between warps in the loop.
+// (Copies by cp.async instead took turns with every other access of the SM:
+// stores and page look-ups waited 3 us and more behind them.)  Tiny pages and
+// strides that no tensor map has take 16-byte copies into the same layout.
+// P's accumulator layout (row = key) becomes the operand layout (row = query
 // row) by movmatrix.  P enters as hi + lo, two bf16 values (relative error
 // 2^-18): a single bf16 would double the output's squared rounding error, and
 // the kernel waits for the cache's bytes, not for these products.
@@ -36,7 +30,10 @@
 // shared: its CTAs write their parts (O unnormalised, m, l) to the workspace
 // and the one that finishes last joins them in CTA order, so the result does
 // not depend on which one that is.
+#include <cuda.h>
+
 #include "attn.cuh"
+#include "tc.cuh"
 
 namespace flint {
 namespace {
@@ -49,10 +46,30 @@ constexpr int kMinWeight = 1;   // least work of a CTA
 constexpr int kChunkBytes = 16 * kHeadDim * 2 * 2;  // 16 keys' K and V
 constexpr float kLazy = 8.0f;
 
+constexpr uint32_t kWaitNs = 200u * 1000 * 1000;
+constexpr int kOPitch = kHeadDim + 4;  // floats; keeps the parts' stores off each other's banks
+
 struct Args {
   AttnArgs a;
   RowsWs w;
+  int box, box_log2;  // rows of a tiled copy: gcd(block_size, 16)
 };
+struct Maps {
+  CUtensorMap k, v;  // {128, heads, slots, pages}, box {64, 1, box, 1}
+};
+
+FLINT_DEV void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+FLINT_DEV void ldmatrix4_trans(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
 
 FLINT_DEV uint32_t movmatrix(uint32_t v) {
   uint32_t r;
@@ -129,7 +146,7 @@ struct Walk {
 
 template <int NT>
 struct Acc {
-  float o[NT][8][4];  // tile j: {dim 8g+j, 64+8g+j} x rows 2t, 2t+1 of 8-row tile nt
+  float o[NT][8][4];  // tile j: dims {16j+g, 16j+8+g} x rows 2t, 2t+1 of 8-row tile nt
   float m[NT][2], l[NT][2];
 };
 
@@ -139,8 +156,9 @@ FLINT_DEV int head_of(const AttnArgs& a, const Part& u, int r) { return u.h * (a
 // The warps' parts of 8 NT rows, joined in warp order.
 template <int NT>
 struct Parts {
-  float o[kRowsWarps][8 * NT][kHeadDim];
+  float o[kRowsWarps][8 * NT][kOPitch];
   float m[kRowsWarps][8 * NT], l[kRowsWarps][8 * NT];
+  uint64_t full[kRowsWarps][3];  // per warp and ring slot: the chunk's bytes are there
   int start[3];
   int last;
   long long pos[2];
@@ -151,7 +169,7 @@ constexpr int kDepth = NT == 1 ? 3 : 2;  // what shared memory holds beside Part
 template <int NT>
 constexpr size_t kRing = (size_t)kDepth<NT> * kRowsWarps * kChunkBytes;
 template <int NT>
-constexpr size_t kSmem = kRing<NT> + sizeof(Parts<NT>);
+constexpr size_t kSmem = kRing<NT> + sizeof(Parts<NT>) + 1024;
 template <int NT>
 constexpr int kPartFloats = 8 * NT * (kHeadDim + 2);
 
@@ -171,12 +189,10 @@ FLINT_DEV void store_part(Parts<NT>& P, const Acc<NT>& A) {
         P.l[warp][r] = l;
       }
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int j = 0; j < 8; j += 4)
-          *reinterpret_cast<float4*>(&P.o[warp][r][64 * i + 8 * g + j]) =
-              make_float4(A.o[nt][j][2 * i + f], A.o[nt][j + 1][2 * i + f], A.o[nt][j + 2][2 * i + f],
-                          A.o[nt][j + 3][2 * i + f]);
+      for (int j = 0; j < 8; ++j) {
+        P.o[warp][r][16 * j + g] = A.o[nt][j][f];
+        P.o[warp][r][16 * j + 8 + g] = A.o[nt][j][2 + f];
+      }
     }
 }
 
@@ -259,40 +275,61 @@ FLINT_DEV bool find_piece(const AttnArgs& a, Parts<NT>& P, Walk<NT>& k) {
   return true;
 }
 
-// GS: keys that lie at one stride (4 where pages have a multiple of 4 slots,
-// else 1), so a look-up of the page table by all lanes serves 2 * GS chunks.
-template <int NT, int GS>
-__global__ void __launch_bounds__(kRowsThreads, 1) attn_rows_kernel(const __grid_constant__ Args args) {
+// TILED: the chunks by tiled copies; otherwise (tiny pages, strides that no
+// tensor map has) by 16-byte copies.
+template <int NT, bool TILED>
+__global__ void __launch_bounds__(kRowsThreads, 1)
+    attn_rows_kernel(const __grid_constant__ Args args, const __grid_constant__ Maps maps) {
   SpanGuard<kSpanAttnRows> span_guard;
-  pdl_wait();  // q and the cache's newest rows are the previous kernel's output
-  pdl_launch_dependents();
-  extern __shared__ __align__(16) uint8_t smem[];
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);  // (stays a shared-memory pointer)
   Parts<NT>& P = *reinterpret_cast<Parts<NT>*>(smem + kRing<NT>);
   const AttnArgs& a = args.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const float c = a.scale * 1.4426950408889634f;
+  if (TILED && lane == 0) {
+    for (int i = 0; i < kDepth<NT>; ++i) mbar_init(&P.full[warp][i], 1);
+    fence_mbar_init();
+  }
+  pdl_wait();  // q and the cache's newest rows are the previous kernel's output
+  pdl_launch_dependents();
 
   Walk<NT> comp;
   if (!find_piece(a, P, comp)) return;
 
-  // ---- the fetch side: a walk of its own, ahead of the products
-  constexpr int kPer = 16 / GS, kChunks = 32 / kPer;  // look-ups per chunk, chunks per look-up
+  // ---- the fetch side: a walk of its own, ahead of the products.  Look-ups of
+  // the page table serve the next kChunks chunks: a lane per box (TILED) or per
+  // key (two chunks)
+  const int per_log2 = TILED ? 4 - args.box_log2 : 4, chunks = 32 >> per_log2;
   Walk<NT> fwalk = comp;
   Part f = {};
-  int ftile = 0, fpos = 0;    // next tile to fetch, its place in the look-up
-  long long cur = -1, nxt = -1;  // element offsets of GS keys each, -1: none
-  uint32_t cur_ok = 0;        // which of them are there
+  int ftile = 0, fpos = 0;  // next tile to fetch, its place in the look-up
+  struct Look {
+    int page, slot;       // page -1: none
+  } cur = {-1, 0}, nxt = {-1, 0};
+  uint32_t cur_ok = 0;      // which of them are there
   bool fmore = true;
   auto chunk_key = [&](int tile) { return tile * kTileKeys + 16 * warp; };
   auto look_up = [&](int tile) {
-    const int at = tile + lane / kPer, key = chunk_key(at) + lane % kPer * GS;
-    return at < f.t1 && key < f.keys ? key_offset(a, f.b, key) : -1ll;
+    const int at = tile + (lane >> per_log2);
+    const int key = chunk_key(at) + ((lane & ((1 << per_log2) - 1)) << (4 - per_log2));
+    Look x = {-1, 0};
+    if (at < f.t1 && key < f.keys) {
+      const int blk = key / a.block_size;
+      x.slot = key - blk * a.block_size;
+      x.page = ldg_cg_i32(a.block_table + (long long)f.b * a.table_stride + blk);
+      if (x.page < 0 || x.page >= a.num_blocks) {
+        attn_error(a.status);
+        x.page = -1;
+      }
+    }
+    return x;
   };
   auto to_chunk = [&]() {  // on to this warp's next chunk, over the units
     if (ftile < f.t1 && chunk_key(ftile) < f.keys) {
-      if (++fpos < kChunks) return;
+      if (++fpos < chunks) return;
       cur = nxt;
-      nxt = look_up(ftile + kChunks);
+      nxt = look_up(ftile + chunks);
     } else {
       do {
         fmore = fwalk.next(a, f);
@@ -300,48 +337,55 @@ __global__ void __launch_bounds__(kRowsThreads, 1) attn_rows_kernel(const __grid
       } while (fmore && (ftile >= f.t1 || chunk_key(ftile) >= f.keys));
       if (!fmore) return;
       cur = look_up(ftile);
-      nxt = look_up(ftile + kChunks);
+      nxt = look_up(ftile + chunks);
     }
     fpos = 0;
-    cur_ok = __ballot_sync(0xffffffffu, cur >= 0);
+    cur_ok = __ballot_sync(0xffffffffu, cur.page >= 0);
   };
-  uint4* ring = reinterpret_cast<uint4*>(smem) + (size_t)warp * kDepth<NT> * (kChunkBytes / 16) + lane;
-  auto fetch = [&](int slot) -> uint32_t {  // fills a slot; which of its GS-key groups are there
+  // chunk: K dims 0 .. 63, K 64 .. 127, V likewise, 16 rows of 128 bytes each,
+  // swizzled as a tiled copy of 128-byte rows does
+  const uint32_t ring = smem_addr(smem) + (uint32_t)(warp * kDepth<NT> * kChunkBytes);
+  auto fetch = [&](int slot) -> uint32_t {  // fills a slot; which of its 16 keys are there
     uint32_t there = 0;
     if (fmore) {
-      const uint32_t dst = smem_addr(ring + slot * (kChunkBytes / 16));
-      const int left = f.keys - chunk_key(ftile), l0 = fpos * kPer;  // keys from the chunk's first on
-      there = (cur_ok >> l0) & ((1u << kPer) - 1u);
-      const uint16_t* kb = a.k + (long long)f.h * a.s_head + 8 * t;
-      const uint16_t* vb = a.v + (long long)f.h * a.s_head + 8 * g;
-      auto place = [&](int key, long long o) { return o + (GS > 1 ? (long long)(key % GS) * a.s_slot : 0ll); };
+      const uint32_t dst = ring + (uint32_t)(slot * kChunkBytes);
+      const int left = f.keys - chunk_key(ftile), l0 = fpos << per_log2;
+      there = left >= 16 ? 0xffffu : (1u << left) - 1u;
+      if (TILED) {
+        const uint32_t good = (cur_ok >> l0) & ((1u << (1 << per_log2)) - 1u);
+        if (good != (1u << (1 << per_log2)) - 1u)  // a box past the end or outside the cache
+          for (int i = 0; i < 16; ++i)
+            if (!((good >> (i >> args.box_log2)) & 1u)) there &= ~(1u << i);
+        const int box = lane >> 2, half = lane & 1;
+        const int page = __shfl_sync(0xffffffffu, cur.page, l0 + (box & ((1 << per_log2) - 1)));
+        const int at = __shfl_sync(0xffffffffu, cur.slot, l0 + (box & ((1 << per_log2) - 1)));
+        if (lane == 0) mbar_arrive_expect_tx(&P.full[warp][slot], (uint32_t)((__popc(good) << args.box_log2) * 512));
+        __syncwarp();
+        if (box < (1 << per_log2) && page >= 0)
+          tc::tma_load_4d(smem + warp * kDepth<NT> * kChunkBytes + slot * kChunkBytes + (lane & 3) * 2048 +
+                              (box << args.box_log2) * 128,
+                          lane & 2 ? &maps.v : &maps.k, 64 * half, f.h, at, page, &P.full[warp][slot]);
+        __syncwarp();
+      } else {
+        there &= cur_ok >> l0;
+        // 16 lanes per key
+        const int hi = lane >> 4, ch = lane & 15;
+        const uint16_t* kb = a.k + (long long)f.h * a.s_head + 8 * ch;
+        const uint16_t* vb = a.v + (long long)f.h * a.s_head + 8 * ch;
+        const long long o = cur.page < 0 ? -1 : (long long)cur.page * a.s_block + (long long)cur.slot * a.s_slot;
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int key = g + 8 * e;
-        const long long o = __shfl_sync(0xffffffffu, cur, l0 + key / GS);
-        const bool ok = o >= 0 && key < left;
-        const uint16_t* src = kb + (ok ? place(key, o) : 0ll);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) cp_async16_or_zero(dst + 512 * (4 * e + i), src + 32 * i, ok);
-      }
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int key = 2 * t + 8 * e;
-        const long long o0 = __shfl_sync(0xffffffffu, cur, l0 + key / GS);
-        const long long o1 = GS > 1 ? o0 : __shfl_sync(0xffffffffu, cur, l0 + key + 1);
-#pragma unroll
-        for (int d = 0; d < 2; ++d) {
-          const long long o = d ? o1 : o0;
-          const bool ok = o >= 0 && key + d < left;
-          const uint16_t* src = vb + (ok ? place(key + d, o) : 0ll);
-#pragma unroll
-          for (int i = 0; i < 2; ++i) cp_async16_or_zero(dst + 512 * (8 + 2 * (2 * e + d) + i), src + 64 * i, ok);
+        for (int i = 0; i < 8; ++i) {
+          const int key = 2 * i + hi;
+          const long long x = __shfl_sync(0xffffffffu, o, l0 + key);
+          const uint32_t to = dst + (uint32_t)((ch >> 3) * 2048 + key * 128 + (((ch & 7) ^ (key & 7)) << 4));
+          cp_async16_or_zero(to, kb + (x < 0 ? 0 : x), x >= 0);
+          cp_async16_or_zero(to + 4096, vb + (x < 0 ? 0 : x), x >= 0);
         }
       }
       ++ftile;
       to_chunk();
     }
-    cp_async_commit();
+    if (!TILED) cp_async_commit();
     return there;
   };
   to_chunk();
@@ -349,6 +393,10 @@ __global__ void __launch_bounds__(kRowsThreads, 1) attn_rows_kernel(const __grid
 #pragma unroll
   for (int i = 0; i < kDepth<NT>; ++i) there[i] = fetch(i);
   int slot = 0;
+  uint32_t phase = 0;
+  // this lane's row and 16-byte column in ldmatrix's four 8 x 8 blocks
+  const uint32_t k_row = (uint32_t)((lane & 7) + 8 * ((lane >> 3) & 1)), k_col = (uint32_t)(lane >> 4);
+  const uint32_t v_row = (uint32_t)((lane & 7) + 8 * (lane >> 4)), v_col = (uint32_t)((lane >> 3) & 1);
 
   Part u;
   while (comp.next(a, u)) {
@@ -358,13 +406,16 @@ __global__ void __launch_bounds__(kRowsThreads, 1) attn_rows_kernel(const __grid
       continue;
     }
     // ---- Q of the unit's rows
-    uint4 qf[NT][4];
+    uint32_t qf[NT][8][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       const bool ok = 8 * nt + g < u.rows;
-      const uint16_t* p = a.q + (long long)u.b * a.q_stride + (long long)head_of(a, u, 8 * nt + g) * kHeadDim + 8 * t;
+      const uint16_t* p = a.q + (long long)u.b * a.q_stride + (long long)head_of(a, u, 8 * nt + g) * kHeadDim + 2 * t;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) qf[nt][i] = ok ? ldg_cg_v4(p + 32 * i) : make_uint4(0, 0, 0, 0);
+      for (int kk = 0; kk < 8; ++kk)
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          qf[nt][kk][e] = ok ? (uint32_t)ldg_cg_i32(reinterpret_cast<const int*>(p + 16 * kk + 8 * e)) : 0u;
     }
     Acc<NT> A;
 #pragma unroll
@@ -380,33 +431,34 @@ __global__ void __launch_bounds__(kRowsThreads, 1) attn_rows_kernel(const __grid
       }
     }
     for (int tile = u.t0; tile < u.t1 && chunk_key(tile) < u.keys; ++tile) {
-      const int key0 = chunk_key(tile);
-      cp_async_wait_group<kDepth<NT> - 1>();
-      const uint4* src = ring + slot * (kChunkBytes / 16);
+      if (TILED) {
+        if (!mbar_test_wait(&P.full[warp][slot], phase)) {
+          const uint32_t t0 = globaltimer_low();
+          while (!mbar_try_wait(&P.full[warp][slot], phase))
+            if (globaltimer_low() - t0 > kWaitNs) {  // (the products go on with what is there)
+              atomicCAS(a.status, 0, FLINT_ERR_TIMEOUT);
+              break;
+            }
+        }
+      } else {
+        cp_async_wait_group<kDepth<NT> - 1>();
+      }
+      __syncwarp();
+      const uint32_t src = ring + (uint32_t)(slot * kChunkBytes);
       const uint32_t ok = there[0];
       float s[NT][4];
-      {
-        uint4 kr[2][4];
 #pragma unroll
-        for (int e = 0; e < 2; ++e)
+      for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) kr[e][i] = src[32 * (4 * e + i)];
+        for (int e = 0; e < 4; ++e) s[nt][e] = 0.0f;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
+      for (int kk = 0; kk < 8; ++kk) {
+        uint32_t kf[4];
+        const uint32_t col = ((2 * kk + k_col) & 7u) ^ (k_row & 7u);
+        ldmatrix4(kf, src + (kk >> 2) * 2048 + k_row * 128 + (col << 4));
 #pragma unroll
-          for (int e = 0; e < 4; ++e) s[nt][e] = 0.0f;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            mma_bf16_16816(s[nt], kr[0][i].x, kr[1][i].x, kr[0][i].y, kr[1][i].y, qf[nt][i].x, qf[nt][i].y);
-            mma_bf16_16816(s[nt], kr[0][i].z, kr[1][i].z, kr[0][i].w, kr[1][i].w, qf[nt][i].z, qf[nt][i].w);
-          }
-        }
+        for (int nt = 0; nt < NT; ++nt) mma_bf16_16816(s[nt], kf[0], kf[1], kf[2], kf[3], qf[nt][kk][0], qf[nt][kk][1]);
       }
-      uint4 vr[4][2];
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-#pragma unroll
-        for (int i = 0; i < 2; ++i) vr[e][i] = src[32 * (8 + 2 * e + i)];
       // s[nt][2 e + i]: key g + 8 e, row 2t + i
       bool raise = false;
 #pragma unroll
@@ -414,7 +466,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1) attn_rows_kernel(const __grid
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int kk = g + 8 * (i >> 1);
-          if (!((ok >> (kk / GS)) & 1u) || key0 + kk >= u.keys) s[nt][i] = neg_inf();
+          if (!((ok >> kk) & 1u)) s[nt][i] = neg_inf();
           raise |= s[nt][i] * c > A.m[nt][i & 1] + kLazy;
         }
       if (__any_sync(0xffffffffu, raise)) {
@@ -455,27 +507,33 @@ __global__ void __launch_bounds__(kRowsThreads, 1) attn_rows_kernel(const __grid
           bl[nt][e] = movmatrix(lo);
         }
       }
+      // V's values where no key is may be anything: P is 0 there, and so are they made
+      const uint32_t vm[2] = {((ok >> (2 * t)) & 1u ? 0xffffu : 0u) | ((ok >> (2 * t + 1)) & 1u ? 0xffff0000u : 0u),
+                              ((ok >> (2 * t + 8)) & 1u ? 0xffffu : 0u) | ((ok >> (2 * t + 9)) & 1u ? 0xffff0000u : 0u)};
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const uint32_t sel = j & 1 ? 0x7632u : 0x5410u;
-        uint32_t av[4];
+        uint32_t vf[4];
+        const uint32_t col = ((2 * j + v_col) & 7u) ^ (v_row & 7u);
+        ldmatrix4_trans(vf, src + 4096 + (j >> 2) * 2048 + v_row * 128 + (col << 4));
+        if (ok != 0xffffu) {
 #pragma unroll
-        for (int e = 0; e < 2; ++e)    // keys 2t, 2t + 1 (+ 8 e)
-#pragma unroll
-          for (int i = 0; i < 2; ++i)  // dims 8g + j, 64 + 8g + j
-            av[2 * e + i] = __byte_perm(reinterpret_cast<const uint32_t*>(&vr[2 * e][i])[j >> 1],
-                                        reinterpret_cast<const uint32_t*>(&vr[2 * e + 1][i])[j >> 1], sel);
+          for (int e = 0; e < 4; ++e) vf[e] &= vm[e >> 1];
+        }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          mma_bf16_16816(A.o[nt][j], av[0], av[1], av[2], av[3], bh[nt][0], bh[nt][1]);
-          mma_bf16_16816(A.o[nt][j], av[0], av[1], av[2], av[3], bl[nt][0], bl[nt][1]);
+          mma_bf16_16816(A.o[nt][j], vf[0], vf[1], vf[2], vf[3], bh[nt][0], bh[nt][1]);
+          mma_bf16_16816(A.o[nt][j], vf[0], vf[1], vf[2], vf[3], bl[nt][0], bl[nt][1]);
         }
       }
-      // the slot's pieces are in registers: fill it again
+      // all lanes have read the slot: fill it again
+      __syncwarp();
 #pragma unroll
       for (int i = 0; i + 1 < kDepth<NT>; ++i) there[i] = there[i + 1];
       there[kDepth<NT> - 1] = fetch(slot);
-      slot = slot + 1 == kDepth<NT> ? 0 : slot + 1;
+      if (++slot == kDepth<NT>) {
+        slot = 0;
+        phase ^= 1u;
+      }
     }
     // ---- the unit's end in this CTA
     store_part<NT>(P, A);
@@ -561,12 +619,12 @@ __global__ void __launch_bounds__(kRowsThreads, 1) attn_rows_kernel(const __grid
     }
     __syncthreads();  // Parts is free again
   }
-  cp_async_wait_all();
+  if (!TILED) cp_async_wait_all();
 }
 
-template <int NT, int GS>
-cudaError_t launch_nt(const AttnArgs& a, const RowsWs& w, cudaStream_t st) {
-  const void* fn = reinterpret_cast<const void*>(attn_rows_kernel<NT, GS>);
+template <int NT, bool TILED>
+cudaError_t launch_nt(const AttnArgs& a, const RowsWs& w, const Maps& maps, int box, cudaStream_t st) {
+  const void* fn = reinterpret_cast<const void*>(attn_rows_kernel<NT, TILED>);
   static std::atomic<bool> allowed[64];
   cudaError_t err = allow_smem(fn, (int)kSmem<NT>, allowed);
   if (err != cudaSuccess) return err;
@@ -586,7 +644,9 @@ cudaError_t launch_nt(const AttnArgs& a, const RowsWs& w, cudaStream_t st) {
   Args p;
   p.a = a;
   p.w = w;
-  void* args[] = {&p};
+  p.box = box;
+  for (p.box_log2 = 0; (1 << p.box_log2) < box;) ++p.box_log2;
+  void* args[] = {&p, const_cast<Maps*>(&maps)};
   return cudaLaunchKernelExC(&cfg, fn, args);
 }
 
@@ -603,11 +663,14 @@ RowsWs rows_ws(void* base) {
 }
 
 cudaError_t launch_attn_rows(const AttnArgs& a, const RowsWs& w, cudaStream_t st) {
+  Maps maps = {};
+  const int box = attn_box(a.block_size, 16);
+  const bool tiled = box >= kAttnMinBox && attn_map(&maps.k, a, a.k, box) && attn_map(&maps.v, a, a.v, box);
   // 8 rows per unit where a group fits them, else 16 (the keys are read once
   // per unit)
-  const bool small = a.nq / a.nkv <= 8;
-  if (a.block_size % 4 == 0) return small ? launch_nt<1, 4>(a, w, st) : launch_nt<2, 4>(a, w, st);
-  return small ? launch_nt<1, 1>(a, w, st) : launch_nt<2, 1>(a, w, st);
+  if (a.nq / a.nkv <= 8)
+    return tiled ? launch_nt<1, true>(a, w, maps, box, st) : launch_nt<1, false>(a, w, maps, box, st);
+  return tiled ? launch_nt<2, true>(a, w, maps, box, st) : launch_nt<2, false>(a, w, maps, box, st);
 }
 
 FLINT_SPAN_SETTER(attn_rows)

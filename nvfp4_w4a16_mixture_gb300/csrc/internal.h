@@ -3,6 +3,7 @@
 
 #include <atomic>
 
+#include <cuda.h>
 #include <cuda_runtime.h>
 #include <stddef.h>
 #include <stdint.h>
@@ -233,6 +234,14 @@ struct AttnArgs {
   float* lse;     // [T, nq] or null
   int* status;
 };
+// Rows of a tiled copy of the cache's slots: the largest power of two up to
+// `most` that divides the page.  Below kAttnMinBox 16-byte copies are faster.
+constexpr int kAttnMinBox = 4;
+int attn_box(int block_size, int most);
+// The map {128 dims, heads, slots, pages} with boxes of {64, 1, box, 1},
+// 128-byte swizzle; false for strides that no tensor map takes.
+bool attn_map(CUtensorMap* m, const AttnArgs& a, const uint16_t* base, int box);
+
 // Workspaces of both attention kernels: the status word, each kernel's
 // counters (zero between calls) at a place of its own, then data.
 constexpr size_t kAttnRowsCounters = 256, kAttnPromptCounters = 1024, kAttnData = 4096;

@@ -120,6 +120,10 @@ DECODE = [
     ([0], 8, 2, 16),
     ([0] * 5 + [30] * 400 + [0, 1000, 0] + [3] * 130, 4, 2, 16),  # more sequences than threads
     ([20000], 8, 1, 16),
+    ([100, 7, 333], 8, 2, 4),
+    ([65, 1], 16, 2, 12),
+    ([130], 4, 4, 2),
+    ([700, 16], 20, 1, 4),
 ]
 
 
@@ -129,6 +133,21 @@ def test_decode(lens, nq, nkv, page):
     p = Problem(lens, [1] * len(lens), nq, nkv, page, seed=len(lens) + nq)
     out, lse = run_decode(p)
     check(out, lse, p.expect(SCALE, P_SPLIT), f"decode {lens[:4]}")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("nq", [8, 64])
+def test_decode_on_a_cache_with_shared_heads(nq):
+    """One stored head read as four (a head stride of 0): no tiled copies."""
+    p = Problem([300, 0, 77], [1] * 3, nq, 1, 16, seed=29)
+    g = p.gpu()
+    g.pop("cu_q")
+    for name in ("k_cache", "v_cache"):
+        g[name] = g[name].expand(-1, -1, 4, -1)
+    p.k, p.v = (c.expand(-1, -1, 4, -1) for c in (p.k, p.v))
+    lse = torch.empty(3, nq, dtype=torch.float32, device="cuda")
+    out = fm.flint_attn_decode(**g, lse=lse)
+    check(out, lse, p.expect(SCALE, P_SPLIT), "shared heads")
 
 
 @pytest.mark.gpu
@@ -287,6 +306,9 @@ PROMPT = [
     ([2300], [9], 8, 2, 48),
     ([40, 41, 42, 43] * 10, [40, 41, 42, 43] * 10, 8, 2, 16),
     ([900, 3], [900, 3], 40, 8, 256),
+    ([300, 60], [300, 10], 8, 2, 4),
+    ([200], [200], 16, 2, 2),
+    ([333, 130], [100, 130], 8, 1, 12),
 ]
 
 
