@@ -161,7 +161,7 @@ struct Parts {
   uint64_t full[kRowsWarps][3];  // per warp and ring slot: the chunk's bytes are there
   int start[3];
   int last;
-  long long pos[2];
+  long long pos;
   long long scan[kRowsWarps];
 };
 template <int NT>
@@ -213,64 +213,87 @@ FLINT_DEV void write_row(const AttnArgs& a, const Part& u, int r, int d4, float4
   if (a.lse && d4 == 0) a.lse[row] = l == 0.0f ? neg_inf() : (m + log2f(l)) * 0.6931471805599453f;
 }
 
-// This CTA's piece of the line: [pos, end) of total, and the unit it starts in.
+// Where position pos of the line of `total` weights begins for CTA c of n.
+FLINT_DEV long long cut(long long c, long long total, long long n) {
+  return total < (1 << 23) ? (long long)((uint32_t)c * (uint32_t)total / (uint32_t)n) : c * total / n;  // (n <= 152)
+}
+
+// This CTA's piece of the line, and the unit it starts in.
 template <int NT>
 FLINT_DEV bool find_piece(const AttnArgs& a, Parts<NT>& P, Walk<NT>& k) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  // two rounds over the sequences: the total, then the start (one round where
-  // all sequences fit the CTA's threads)
   long long total = 0, pos = -1, end = 0;
   k.units = (a.nq / a.nkv + 8 * NT - 1) / (8 * NT) * a.nkv;
-  for (int round = 0; round < 2; ++round) {
-    long long base = 0;
-    for (int b0 = 0; b0 < a.B; b0 += kRowsThreads) {
-      const int b = b0 + tid;
-      long long w = 0;
-      int tiles = 0;
-      if (b < a.B) {
-        tiles = (seq_keys(a, b) + kTileKeys - 1) / kTileKeys;
-        w = (long long)k.units * (tiles + kUnitWeight);
-      }
-      long long x = w;
+  auto weight = [&](int b, int& w) {  // of sequence b, and of one of its units
+    w = 1;
+    if (b >= a.B) return 0ll;
+    w = (seq_keys(a, b) + kTileKeys - 1) / kTileKeys + kUnitWeight;
+    return (long long)k.units * w;
+  };
+  auto scan = [&](long long x) {  // over the lanes, inclusive
 #pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const long long y = __shfl_up_sync(0xffffffffu, x, d);
-        if (lane >= d) x += y;
-      }
-      __syncthreads();
-      if (lane == 31) P.scan[warp] = x;
-      __syncthreads();
-      long long below = base;
-#pragma unroll
-      for (int i = 0; i < kRowsWarps; ++i) {
-        if (i < warp) below += P.scan[i];
-        base += P.scan[i];
-      }
-      const long long first = below + x - w;
-      if (round == 0 && b0 + kRowsThreads >= a.B) {
-        total = base;
-        const long long ctas = total == 0 ? 0 : max(1ll, min((long long)gridDim.x, total / kMinWeight));
-        k.total = total;
-        k.ctas = ctas;
-        if ((long long)blockIdx.x >= ctas) return false;
-        pos = blockIdx.x * total / ctas;
-        end = (blockIdx.x + 1) * total / ctas;
-      }
-      if (pos >= first && pos < first + w) {
-        P.start[0] = b;
-        P.start[1] = (int)((pos - first) / (tiles + kUnitWeight));
-        P.start[2] = (int)((pos - first) % (tiles + kUnitWeight));
-        P.pos[0] = first;
-      }
+    for (int d = 1; d < 32; d <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, x, d);
+      if (lane >= d) x += y;
     }
-    if (a.B <= kRowsThreads) break;
+    return x;
+  };
+  auto piece = [&]() {
+    k.total = total;
+    k.ctas = total == 0 ? 0 : max(1ll, min((long long)gridDim.x, total / kMinWeight));
+    if ((long long)blockIdx.x >= k.ctas) return false;
+    pos = cut(blockIdx.x, total, k.ctas);
+    end = cut(blockIdx.x + 1, total, k.ctas);
+    return true;
+  };
+  if (a.B <= 32) {  // every warp for itself
+    int w;
+    const long long mine = weight(lane, w), upto = scan(mine), first = upto - mine;
+    total = __shfl_sync(0xffffffffu, upto, 31);
+    if (!piece()) return false;
+    const int src = __ffs(__ballot_sync(0xffffffffu, pos >= first && pos < upto)) - 1;
+    k.b = src;
+    k.at = __shfl_sync(0xffffffffu, first, src);
+    w = __shfl_sync(0xffffffffu, w, src);
+    k.unit = (int)((pos - k.at) / w);
+    k.off = (int)((pos - k.at) % w);
+  } else {
+    // two rounds over the sequences: the total, then the start (one round where
+    // all sequences fit the CTA's threads)
+    for (int round = 0; round < 2; ++round) {
+      long long base = 0;
+      for (int b0 = 0; b0 < a.B; b0 += kRowsThreads) {
+        int w;
+        const long long mine = weight(b0 + tid, w), upto = scan(mine);
+        __syncthreads();
+        if (lane == 31) P.scan[warp] = upto;
+        __syncthreads();
+        long long first = base + upto - mine;
+#pragma unroll
+        for (int i = 0; i < kRowsWarps; ++i) {
+          if (i < warp) first += P.scan[i];
+          base += P.scan[i];
+        }
+        if (round == 0 && b0 + kRowsThreads >= a.B) {
+          total = base;
+          if (!piece()) return false;
+        }
+        if (pos >= first && pos < first + mine) {
+          P.start[0] = b0 + tid;
+          P.start[1] = (int)((pos - first) / w);
+          P.start[2] = (int)((pos - first) % w);
+          P.pos = first;
+        }
+      }
+      if (a.B <= kRowsThreads) break;
+    }
+    __syncthreads();
+    k.b = P.start[0];
+    k.unit = P.start[1];
+    k.off = P.start[2];
+    k.at = P.pos;
   }
-  __syncthreads();
   k.rem = end - pos;
-  k.b = P.start[0];
-  k.unit = P.start[1];
-  k.off = P.start[2];
-  k.at = P.pos[0];
   k.sequence(a);
   return true;
 }
@@ -297,11 +320,30 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
   Walk<NT> comp;
   if (!find_piece(a, P, comp)) return;
 
+  // Q of the next unit's rows, asked for before the keys' copies fill the
+  // memory's queues (behind them it took 5 us and more)
+  uint32_t qf[NT][8][2];
+  auto load_q = [&](const Part& x) {
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const bool ok = 8 * nt + g < x.rows;
+      const uint16_t* p = a.q + (long long)x.b * a.q_stride + (long long)head_of(a, x, 8 * nt + g) * kHeadDim + 2 * t;
+#pragma unroll
+      for (int kk = 0; kk < 8; ++kk)
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          qf[nt][kk][e] = ok ? (uint32_t)ldg_cg_i32(reinterpret_cast<const int*>(p + 16 * kk + 8 * e)) : 0u;
+    }
+  };
+  Walk<NT> fwalk = comp;
+  Part coming;
+  bool more = comp.next(a, coming);
+  if (more) load_q(coming);
+
   // ---- the fetch side: a walk of its own, ahead of the products.  Look-ups of
   // the page table serve the next kChunks chunks: a lane per box (TILED) or per
   // key (two chunks)
   const int per_log2 = TILED ? 4 - args.box_log2 : 4, chunks = 32 >> per_log2;
-  Walk<NT> fwalk = comp;
   Part f = {};
   int ftile = 0, fpos = 0;  // next tile to fetch, its place in the look-up
   struct Look {
@@ -398,24 +440,14 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
   const uint32_t k_row = (uint32_t)((lane & 7) + 8 * ((lane >> 3) & 1)), k_col = (uint32_t)(lane >> 4);
   const uint32_t v_row = (uint32_t)((lane & 7) + 8 * (lane >> 4)), v_col = (uint32_t)((lane >> 3) & 1);
 
-  Part u;
-  while (comp.next(a, u)) {
+  while (more) {
+    const Part u = coming;
     if (u.t0 >= u.t1) {  // a sequence without keys
       for (int i = threadIdx.x; i < u.rows * 32; i += kRowsThreads)
         write_row(a, u, i >> 5, i & 31, make_float4(0.0f, 0.0f, 0.0f, 0.0f), 0.0f, 0.0f);
+      more = comp.next(a, coming);
+      if (more) load_q(coming);
       continue;
-    }
-    // ---- Q of the unit's rows
-    uint32_t qf[NT][8][2];
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      const bool ok = 8 * nt + g < u.rows;
-      const uint16_t* p = a.q + (long long)u.b * a.q_stride + (long long)head_of(a, u, 8 * nt + g) * kHeadDim + 2 * t;
-#pragma unroll
-      for (int kk = 0; kk < 8; ++kk)
-#pragma unroll
-        for (int e = 0; e < 2; ++e)
-          qf[nt][kk][e] = ok ? (uint32_t)ldg_cg_i32(reinterpret_cast<const int*>(p + 16 * kk + 8 * e)) : 0u;
     }
     Acc<NT> A;
 #pragma unroll
@@ -536,6 +568,8 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
       }
     }
     // ---- the unit's end in this CTA
+    more = comp.next(a, coming);
+    if (more) load_q(coming);
     store_part<NT>(P, A);
     __syncthreads();
     const bool whole = u.c_first == u.c_last;
@@ -587,30 +621,43 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
           const int x = u.c_first + i;
           return args.w.parts + (size_t)(2 * x + (i == 0)) * kPartFloats<NT>;
         };
+        constexpr int kMost = (kRowsCtas + 31) / 32;
         for (int r = warp; r < u.rows; r += kRowsWarps) {
-          float m = neg_inf();
-          for (int i = lane; i < n; i += 32) m = fmaxf(m, __ldcg(part_at(i) + 8 * NT * kHeadDim + r));
+          float pm[kMost], pl[kMost], m = neg_inf();
+#pragma unroll
+          for (int x = 0; x < kMost; ++x) {
+            const int i = 32 * x + lane;
+            pm[x] = i < n ? __ldcg(part_at(i) + 8 * NT * kHeadDim + r) : neg_inf();
+            pl[x] = i < n ? __ldcg(part_at(i) + 8 * NT * (kHeadDim + 1) + r) : 0.0f;
+          }
+#pragma unroll
+          for (int x = 0; x < kMost; ++x) m = fmaxf(m, pm[x]);
 #pragma unroll
           for (int d = 16; d >= 1; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
           float l = 0.0f;
           float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-          for (int i0 = 0; i0 < n; i0 += 32) {
-            float y = 0.0f, yl = 0.0f;
-            if (i0 + lane < n) {
-              const float pl = __ldcg(part_at(i0 + lane) + 8 * NT * (kHeadDim + 1) + r);
-              y = part_factor(__ldcg(part_at(i0 + lane) + 8 * NT * kHeadDim + r), pl, m);
-              yl = y * pl;
-            }
-            const int here = min(32, n - i0);
-#pragma unroll 8
-            for (int i = 0; i < here; ++i) {
-              const float f = __shfl_sync(0xffffffffu, y, i);
-              l += __shfl_sync(0xffffffffu, yl, i);
-              const float4 v = __ldcg(reinterpret_cast<const float4*>(part_at(i0 + i) + r * kHeadDim + 4 * lane));
-              o.x += f * v.x;
-              o.y += f * v.y;
-              o.z += f * v.z;
-              o.w += f * v.w;
+#pragma unroll
+          for (int x = 0; x < kMost; ++x) {
+            const float y = part_factor(pm[x], pl[x], m), yl = y * pl[x];
+            const int here = min(32, n - 32 * x);
+            for (int i0 = 0; i0 < here; i0 += 16) {
+              float4 v[16];
+#pragma unroll
+              for (int i = 0; i < 16; ++i)
+                v[i] = i0 + i < here
+                           ? __ldcg(reinterpret_cast<const float4*>(part_at(32 * x + i0 + i) + r * kHeadDim + 4 * lane))
+                           : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+              for (int i = 0; i < 16; ++i) {
+                const float f = __shfl_sync(0xffffffffu, y, i0 + i);
+                l += __shfl_sync(0xffffffffu, yl, i0 + i);
+                if (i0 + i < here) {
+                  o.x += f * v[i].x;
+                  o.y += f * v[i].y;
+                  o.z += f * v[i].z;
+                  o.w += f * v[i].w;
+                }
+              }
             }
           }
           write_row(a, u, r, lane, o, m, l);
