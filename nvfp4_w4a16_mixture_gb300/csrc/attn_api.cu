@@ -53,6 +53,8 @@ int attention(bool prompt, const void* q, long long q_stride, const flint_kv_cac
   if (q_stride < 0 || q_stride % 8 != 0) return FLINT_ERR_INVALID_ARG;
   if (prompt && (!cu_q || !aligned(cu_q, 4))) return FLINT_ERR_INVALID_ARG;
   if ((long long)T * nq > kMaxKeys) return FLINT_ERR_UNSUPPORTED;
+  // (a sequence's tiles over all heads stay below 2^31)
+  if ((long long)max_blocks * cache->block_size / 128 * nq > (long long)kMaxKeys) return FLINT_ERR_UNSUPPORTED;
   if (!workspace || !aligned(workspace, 256) || workspace_bytes < need) return FLINT_ERR_WORKSPACE;
   AttnArgs a = {};
   a.q = static_cast<const uint16_t*>(q);

@@ -91,6 +91,17 @@ struct Part {
   int c_first, c_last;  // CTAs that share the unit
 };
 
+// The line of `total` weights is cut into n pieces (n <= 152): piece c begins
+// at floor(c total / n), position x lies in piece floor(((x + 1) n - 1) /
+// total).  32-bit arithmetic where it fits (a 64-bit division takes 0.3 us).
+FLINT_DEV long long cut(long long c, long long total, long long n) {
+  return total < (1 << 23) ? (long long)((uint32_t)c * (uint32_t)total / (uint32_t)n) : c * total / n;
+}
+FLINT_DEV int piece_of(long long x, long long total, long long n) {
+  return total < (1 << 23) ? (int)((((uint32_t)x + 1u) * (uint32_t)n - 1u) / (uint32_t)total)
+                           : (int)(((x + 1) * n - 1) / total);
+}
+
 // A walk along the CTA's piece of the line.
 template <int NT>
 struct Walk {
@@ -103,6 +114,8 @@ struct Walk {
     keys = seq_keys(a, b);
     tiles = (keys + kTileKeys - 1) / kTileKeys;
   }
+  // SHARERS: whether the CTAs that share the unit are wanted
+  template <bool SHARERS>
   FLINT_DEV bool next(const AttnArgs& a, Part& p) {
     while (rem > 0) {
       if (unit == units) {
@@ -126,10 +139,10 @@ struct Walk {
         p.t0 = min(off, tiles);
         p.t1 = min(off + take, tiles);
         p.c_first = p.c_last = blockIdx.x;
-        if (off > 0 || take < real) {  // CTA of position x: floor(((x + 1) ctas - 1) / total)
+        if (SHARERS && (off > 0 || take < real)) {
           const long long u0 = at + (long long)unit * w;
-          p.c_first = (int)(((u0 + 1) * ctas - 1) / total);
-          p.c_last = (int)(((u0 + real) * ctas - 1) / total);
+          p.c_first = piece_of(u0, total, ctas);
+          p.c_last = piece_of(u0 + real - 1, total, ctas);
         }
       }
       rem -= take;
@@ -213,11 +226,6 @@ FLINT_DEV void write_row(const AttnArgs& a, const Part& u, int r, int d4, float4
   if (a.lse && d4 == 0) a.lse[row] = l == 0.0f ? neg_inf() : (m + log2f(l)) * 0.6931471805599453f;
 }
 
-// Where position pos of the line of `total` weights begins for CTA c of n.
-FLINT_DEV long long cut(long long c, long long total, long long n) {
-  return total < (1 << 23) ? (long long)((uint32_t)c * (uint32_t)total / (uint32_t)n) : c * total / n;  // (n <= 152)
-}
-
 // This CTA's piece of the line, and the unit it starts in.
 template <int NT>
 FLINT_DEV bool find_piece(const AttnArgs& a, Parts<NT>& P, Walk<NT>& k) {
@@ -255,8 +263,9 @@ FLINT_DEV bool find_piece(const AttnArgs& a, Parts<NT>& P, Walk<NT>& k) {
     k.b = src;
     k.at = __shfl_sync(0xffffffffu, first, src);
     w = __shfl_sync(0xffffffffu, w, src);
-    k.unit = (int)((pos - k.at) / w);
-    k.off = (int)((pos - k.at) % w);
+    const uint32_t in = (uint32_t)(pos - k.at);  // (a sequence's weight is below 2^31: heads x tiles)
+    k.unit = (int)(in / (uint32_t)w);
+    k.off = (int)(in % (uint32_t)w);
   } else {
     // two rounds over the sequences: the total, then the start (one round where
     // all sequences fit the CTA's threads)
@@ -280,8 +289,9 @@ FLINT_DEV bool find_piece(const AttnArgs& a, Parts<NT>& P, Walk<NT>& k) {
         }
         if (pos >= first && pos < first + mine) {
           P.start[0] = b0 + tid;
-          P.start[1] = (int)((pos - first) / w);
-          P.start[2] = (int)((pos - first) % w);
+          const uint32_t in = (uint32_t)(pos - first);
+          P.start[1] = (int)(in / (uint32_t)w);
+          P.start[2] = (int)(in % (uint32_t)w);
           P.pos = first;
         }
       }
@@ -320,8 +330,8 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
   Walk<NT> comp;
   if (!find_piece(a, P, comp)) return;
 
-  // Q of the next unit's rows, asked for before the keys' copies fill the
-  // memory's queues (behind them it took 5 us and more)
+  // Q of the next unit's rows.  It and the first look-ups are asked for before
+  // the keys' copies fill the memory's queues: behind those they took 5 us
   uint32_t qf[NT][8][2];
   auto load_q = [&](const Part& x) {
 #pragma unroll
@@ -335,54 +345,58 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
           qf[nt][kk][e] = ok ? (uint32_t)ldg_cg_i32(reinterpret_cast<const int*>(p + 16 * kk + 8 * e)) : 0u;
     }
   };
-  Walk<NT> fwalk = comp;
-  Part coming;
-  bool more = comp.next(a, coming);
-  if (more) load_q(coming);
-
   // ---- the fetch side: a walk of its own, ahead of the products.  Look-ups of
   // the page table serve the next kChunks chunks: a lane per box (TILED) or per
   // key (two chunks)
   const int per_log2 = TILED ? 4 - args.box_log2 : 4, chunks = 32 >> per_log2;
+  Walk<NT> fwalk = comp;
   Part f = {};
   int ftile = 0, fpos = 0;  // next tile to fetch, its place in the look-up
   struct Look {
-    int page, slot;       // page -1: none
-  } cur = {-1, 0}, nxt = {-1, 0};
-  uint32_t cur_ok = 0;      // which of them are there
+    int page, slot;  // page kNone: no such key
+  };
+  constexpr int kNone = -0x7fffffff - 1;
+  Look cur = {kNone, 0}, nxt = {kNone, 0};
+  uint32_t cur_ok = 0;  // which of them are in the cache
   bool fmore = true;
   auto chunk_key = [&](int tile) { return tile * kTileKeys + 16 * warp; };
-  auto look_up = [&](int tile) {
+  auto look_up = [&](int tile) {  // (the entry is only waited for in settle)
     const int at = tile + (lane >> per_log2);
     const int key = chunk_key(at) + ((lane & ((1 << per_log2) - 1)) << (4 - per_log2));
-    Look x = {-1, 0};
+    Look x = {kNone, 0};
     if (at < f.t1 && key < f.keys) {
       const int blk = key / a.block_size;
       x.slot = key - blk * a.block_size;
       x.page = ldg_cg_i32(a.block_table + (long long)f.b * a.table_stride + blk);
-      if (x.page < 0 || x.page >= a.num_blocks) {
-        attn_error(a.status);
-        x.page = -1;
-      }
     }
     return x;
   };
-  auto to_chunk = [&]() {  // on to this warp's next chunk, over the units
+  auto settle = [&]() {
+    fpos = 0;
+    const bool in = cur.page >= 0 && cur.page < a.num_blocks;
+    if (!in && cur.page != kNone) attn_error(a.status);
+    cur_ok = __ballot_sync(0xffffffffu, in);
+  };
+  auto next_part = [&]() {  // on to the next unit in which this warp has a chunk, its look-ups asked for
+    do {
+      fmore = fwalk.template next<false>(a, f);
+      ftile = f.t0;
+    } while (fmore && (ftile >= f.t1 || chunk_key(ftile) >= f.keys));
+    if (fmore) {
+      cur = look_up(ftile);
+      nxt = look_up(ftile + chunks);
+    }
+  };
+  auto to_chunk = [&]() {  // on to this warp's next chunk
     if (ftile < f.t1 && chunk_key(ftile) < f.keys) {
       if (++fpos < chunks) return;
       cur = nxt;
       nxt = look_up(ftile + chunks);
     } else {
-      do {
-        fmore = fwalk.next(a, f);
-        ftile = f.t0;
-      } while (fmore && (ftile >= f.t1 || chunk_key(ftile) >= f.keys));
+      next_part();
       if (!fmore) return;
-      cur = look_up(ftile);
-      nxt = look_up(ftile + chunks);
     }
-    fpos = 0;
-    cur_ok = __ballot_sync(0xffffffffu, cur.page >= 0);
+    settle();
   };
   // chunk: K dims 0 .. 63, K 64 .. 127, V likewise, 16 rows of 128 bytes each,
   // swizzled as a tiled copy of 128-byte rows does
@@ -403,7 +417,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
         const int at = __shfl_sync(0xffffffffu, cur.slot, l0 + (box & ((1 << per_log2) - 1)));
         if (lane == 0) mbar_arrive_expect_tx(&P.full[warp][slot], (uint32_t)((__popc(good) << args.box_log2) * 512));
         __syncwarp();
-        if (box < (1 << per_log2) && page >= 0)
+        if (box < (1 << per_log2) && ((good >> box) & 1u))
           tc::tma_load_4d(smem + warp * kDepth<NT> * kChunkBytes + slot * kChunkBytes + (lane & 3) * 2048 +
                               (box << args.box_log2) * 128,
                           lane & 2 ? &maps.v : &maps.k, 64 * half, f.h, at, page, &P.full[warp][slot]);
@@ -414,7 +428,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
         const int hi = lane >> 4, ch = lane & 15;
         const uint16_t* kb = a.k + (long long)f.h * a.s_head + 8 * ch;
         const uint16_t* vb = a.v + (long long)f.h * a.s_head + 8 * ch;
-        const long long o = cur.page < 0 ? -1 : (long long)cur.page * a.s_block + (long long)cur.slot * a.s_slot;
+        const long long o = !((cur_ok >> lane) & 1u) ? -1 : (long long)cur.page * a.s_block + (long long)cur.slot * a.s_slot;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const int key = 2 * i + hi;
@@ -430,7 +444,11 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
     if (!TILED) cp_async_commit();
     return there;
   };
-  to_chunk();
+  next_part();
+  Part coming;
+  bool more = comp.template next<true>(a, coming);
+  if (more) load_q(coming);
+  if (fmore) settle();
   uint32_t there[kDepth<NT>];
 #pragma unroll
   for (int i = 0; i < kDepth<NT>; ++i) there[i] = fetch(i);
@@ -445,7 +463,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
     if (u.t0 >= u.t1) {  // a sequence without keys
       for (int i = threadIdx.x; i < u.rows * 32; i += kRowsThreads)
         write_row(a, u, i >> 5, i & 31, make_float4(0.0f, 0.0f, 0.0f, 0.0f), 0.0f, 0.0f);
-      more = comp.next(a, coming);
+      more = comp.template next<true>(a, coming);
       if (more) load_q(coming);
       continue;
     }
@@ -568,7 +586,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
       }
     }
     // ---- the unit's end in this CTA
-    more = comp.next(a, coming);
+    more = comp.template next<true>(a, coming);
     if (more) load_q(coming);
     store_part<NT>(P, A);
     __syncthreads();
