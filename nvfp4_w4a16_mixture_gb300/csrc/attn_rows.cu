@@ -110,8 +110,8 @@ struct Walk {
   int b, unit, off;
   int keys, tiles, units;  // of the sequence; units is the same for all
 
-  FLINT_DEV void sequence(const AttnArgs& a) {
-    keys = seq_keys(a, b);
+  FLINT_DEV void sequence(int n) {
+    keys = n;
     tiles = (keys + kTileKeys - 1) / kTileKeys;
   }
   // SHARERS: whether the CTAs that share the unit are wanted
@@ -122,7 +122,7 @@ struct Walk {
         at += (long long)units * (tiles + kUnitWeight);
         ++b;
         unit = 0;
-        sequence(a);
+        sequence(seq_keys(a, b));
         continue;
       }
       const int w = tiles + kUnitWeight;
@@ -172,7 +172,7 @@ struct Parts {
   float o[kRowsWarps][8 * NT][kOPitch];
   float m[kRowsWarps][8 * NT], l[kRowsWarps][8 * NT];
   uint64_t full[kRowsWarps][3];  // per warp and ring slot: the chunk's bytes are there
-  int start[3];
+  int start[4];
   int last;
   long long pos;
   long long scan[kRowsWarps];
@@ -232,11 +232,10 @@ FLINT_DEV bool find_piece(const AttnArgs& a, Parts<NT>& P, Walk<NT>& k) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   long long total = 0, pos = -1, end = 0;
   k.units = (a.nq / a.nkv + 8 * NT - 1) / (8 * NT) * a.nkv;
-  auto weight = [&](int b, int& w) {  // of sequence b, and of one of its units
-    w = 1;
-    if (b >= a.B) return 0ll;
-    w = (seq_keys(a, b) + kTileKeys - 1) / kTileKeys + kUnitWeight;
-    return (long long)k.units * w;
+  auto weight = [&](int b, int& keys, int& w) {  // of sequence b, its keys, and the weight of one of its units
+    keys = b < a.B ? seq_keys(a, b) : 0;
+    w = (keys + kTileKeys - 1) / kTileKeys + kUnitWeight;
+    return b < a.B ? (long long)k.units * w : 0ll;
   };
   auto scan = [&](long long x) {  // over the lanes, inclusive
 #pragma unroll
@@ -254,57 +253,45 @@ FLINT_DEV bool find_piece(const AttnArgs& a, Parts<NT>& P, Walk<NT>& k) {
     end = cut(blockIdx.x + 1, total, k.ctas);
     return true;
   };
-  if (a.B <= 32) {  // every warp for itself
-    int w;
-    const long long mine = weight(lane, w), upto = scan(mine), first = upto - mine;
-    total = __shfl_sync(0xffffffffu, upto, 31);
-    if (!piece()) return false;
-    const int src = __ffs(__ballot_sync(0xffffffffu, pos >= first && pos < upto)) - 1;
-    k.b = src;
-    k.at = __shfl_sync(0xffffffffu, first, src);
-    w = __shfl_sync(0xffffffffu, w, src);
-    const uint32_t in = (uint32_t)(pos - k.at);  // (a sequence's weight is below 2^31: heads x tiles)
-    k.unit = (int)(in / (uint32_t)w);
-    k.off = (int)(in % (uint32_t)w);
-  } else {
-    // two rounds over the sequences: the total, then the start (one round where
-    // all sequences fit the CTA's threads)
-    for (int round = 0; round < 2; ++round) {
-      long long base = 0;
-      for (int b0 = 0; b0 < a.B; b0 += kRowsThreads) {
-        int w;
-        const long long mine = weight(b0 + tid, w), upto = scan(mine);
-        __syncthreads();
-        if (lane == 31) P.scan[warp] = upto;
-        __syncthreads();
-        long long first = base + upto - mine;
+  // Two rounds over the sequences: the total, then the start (one round where
+  // all sequences fit the CTA's threads).  Each length is read by one thread of
+  // a CTA: a line that all warps of all CTAs read is served one by one.
+  for (int round = 0; round < 2; ++round) {
+    long long base = 0;
+    for (int b0 = 0; b0 < a.B; b0 += kRowsThreads) {
+      int keys, w;
+      const long long mine = weight(b0 + tid, keys, w), upto = scan(mine);
+      __syncthreads();
+      if (lane == 31) P.scan[warp] = upto;
+      __syncthreads();
+      long long first = base + upto - mine;
 #pragma unroll
-        for (int i = 0; i < kRowsWarps; ++i) {
-          if (i < warp) first += P.scan[i];
-          base += P.scan[i];
-        }
-        if (round == 0 && b0 + kRowsThreads >= a.B) {
-          total = base;
-          if (!piece()) return false;
-        }
-        if (pos >= first && pos < first + mine) {
-          P.start[0] = b0 + tid;
-          const uint32_t in = (uint32_t)(pos - first);
-          P.start[1] = (int)(in / (uint32_t)w);
-          P.start[2] = (int)(in % (uint32_t)w);
-          P.pos = first;
-        }
+      for (int i = 0; i < kRowsWarps; ++i) {
+        if (i < warp) first += P.scan[i];
+        base += P.scan[i];
       }
-      if (a.B <= kRowsThreads) break;
+      if (round == 0 && b0 + kRowsThreads >= a.B) {
+        total = base;
+        if (!piece()) return false;
+      }
+      if (pos >= first && pos < first + mine) {
+        const uint32_t in = (uint32_t)(pos - first);  // (a sequence's weight is below 2^31)
+        P.start[0] = b0 + tid;
+        P.start[1] = (int)(in / (uint32_t)w);
+        P.start[2] = (int)(in % (uint32_t)w);
+        P.start[3] = keys;
+        P.pos = first;
+      }
     }
-    __syncthreads();
-    k.b = P.start[0];
-    k.unit = P.start[1];
-    k.off = P.start[2];
-    k.at = P.pos;
+    if (a.B <= kRowsThreads) break;
   }
+  __syncthreads();
+  k.b = P.start[0];
+  k.unit = P.start[1];
+  k.off = P.start[2];
+  k.at = P.pos;
   k.rem = end - pos;
-  k.sequence(a);
+  k.sequence(P.start[3]);
   return true;
 }
 
@@ -330,21 +317,40 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
   Walk<NT> comp;
   if (!find_piece(a, P, comp)) return;
 
-  // Q of the next unit's rows.  It and the first look-ups are asked for before
-  // the keys' copies fill the memory's queues: behind those they took 5 us
-  uint32_t qf[NT][8][2];
-  auto load_q = [&](const Part& x) {
+  // Q of a unit's rows: 16 bytes per thread (and 8-row tile, half of the
+  // threads), read once per CTA and handed to the warps' fragments through
+  // shared memory (the warps reading it themselves, 4 bytes a lane, made the
+  // rows' few lines a bottleneck: 2 to 4 us).  It and the first look-ups are
+  // asked for before the keys' copies fill the memory's queues.
+  uint4 q_new[NT];
+  auto ask_q = [&](const Part& x) {
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      const bool ok = 8 * nt + g < x.rows;
-      const uint16_t* p = a.q + (long long)x.b * a.q_stride + (long long)head_of(a, x, 8 * nt + g) * kHeadDim + 2 * t;
+      const int r = 8 * nt + (threadIdx.x >> 4), ch = threadIdx.x & 15;
+      q_new[nt] = threadIdx.x < 128 && r < x.rows
+                      ? ldg_cg_v4(a.q + (long long)x.b * a.q_stride + (long long)head_of(a, x, r) * kHeadDim + 8 * ch)
+                      : make_uint4(0, 0, 0, 0);
+    }
+  };
+  uint32_t qf[NT][8][2];
+  auto take_q = [&]() {  // (Parts' first rows are free; the caller's barrier follows)
+    uint16_t* sq = reinterpret_cast<uint16_t*>(&P.o[0][0][0]);
+    constexpr int kPitch = kHeadDim + 8;
+    if (threadIdx.x < 128) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+        *reinterpret_cast<uint4*>(sq + (8 * nt + (threadIdx.x >> 4)) * kPitch + 8 * (threadIdx.x & 15)) = q_new[nt];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int kk = 0; kk < 8; ++kk)
 #pragma unroll
         for (int e = 0; e < 2; ++e)
-          qf[nt][kk][e] = ok ? (uint32_t)ldg_cg_i32(reinterpret_cast<const int*>(p + 16 * kk + 8 * e)) : 0u;
-    }
+          qf[nt][kk][e] = *reinterpret_cast<const uint32_t*>(sq + (8 * nt + g) * kPitch + 16 * kk + 8 * e + 2 * t);
   };
+
   // ---- the fetch side: a walk of its own, ahead of the products.  Look-ups of
   // the page table serve the next kChunks chunks: a lane per box (TILED) or per
   // key (two chunks)
@@ -447,7 +453,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
   next_part();
   Part coming;
   bool more = comp.template next<true>(a, coming);
-  if (more) load_q(coming);
+  if (more) ask_q(coming);
   if (fmore) settle();
   uint32_t there[kDepth<NT>];
 #pragma unroll
@@ -464,9 +470,10 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
       for (int i = threadIdx.x; i < u.rows * 32; i += kRowsThreads)
         write_row(a, u, i >> 5, i & 31, make_float4(0.0f, 0.0f, 0.0f, 0.0f), 0.0f, 0.0f);
       more = comp.template next<true>(a, coming);
-      if (more) load_q(coming);
+      if (more) ask_q(coming);
       continue;
     }
+    take_q();
     Acc<NT> A;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -587,7 +594,8 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
     }
     // ---- the unit's end in this CTA
     more = comp.template next<true>(a, coming);
-    if (more) load_q(coming);
+    if (more) ask_q(coming);
+    __syncthreads();  // all warps have taken Q
     store_part<NT>(P, A);
     __syncthreads();
     const bool whole = u.c_first == u.c_last;
