@@ -2,17 +2,24 @@
 // plan of a compaction.
 //
 // Copy: bytes only.  A (pair, K or V, slot, head) row is 256 contiguous
-// bytes, 16 threads x 16 bytes.
-// Plan: three kernels.  mark sets the bit of every page in use; rank scans
-// the bitmap (one CTA): the live count, each word's number of live pages
-// below it, and the pairs; rename writes the new table.  All in integers, so
-// the result does not depend on the order of the atomics.
+// bytes, 16 threads x 16 bytes; a CTA takes 64 rows of a pair's keys and
+// values at a time, eight 16-byte loads of each thread under way before the
+// first store, and asks for the next pair's page ids meanwhile.
+// Plan: two kernels.  The first sets the bit of every page in use, and its
+// last CTA scans the bitmap: the live count, each word's number of live pages
+// below it, and the pairs; it leaves a copy of the bitmap for the second and
+// the bitmap itself cleared for the next call.  The second writes the new
+// table and fills up the list of pairs.  All in integers, so the result does
+// not depend on the order of the atomics.
 #include "attn.cuh"
 
 namespace flint {
 namespace {
 
 constexpr int kCopyThreads = 256;
+constexpr int kRowStep = kCopyThreads / 16;      // rows that the CTA's threads cover at once
+constexpr int kRowsPer = 4;                      // rows of a thread
+constexpr int kCopyRows = kRowStep * kRowsPer;   // rows of an item
 constexpr int kPlanThreads = 1024;
 
 __global__ void __launch_bounds__(kCopyThreads) kv_copy_kernel(const KvCopyArgs a) {
@@ -21,53 +28,68 @@ __global__ void __launch_bounds__(kCopyThreads) kv_copy_kernel(const KvCopyArgs 
   pdl_launch_dependents();
   int n = a.num_moves;
   if (a.count) n = min(n, ldg_cg_i32(a.count));
-  for (int i = blockIdx.x; i < n; i += gridDim.x) {
-    const int src = ldg_cg_i32(a.moves + 2 * (long long)i), dst = ldg_cg_i32(a.moves + 2 * (long long)i + 1);
-    if (src < 0 || src >= a.num_blocks || dst < 0 || dst >= a.num_blocks) {
-      if (threadIdx.x == 0) attn_error(a.status);
-      continue;
+  const int rows = a.block_size * a.nkv;
+  const int parts = (rows + kCopyRows - 1) / kCopyRows;  // per pair
+  const int step_slot = kRowStep / a.nkv, step_head = kRowStep % a.nkv;
+  const long long items = (long long)max(n, 0) * parts;
+  struct Move {
+    int src, dst, tokens;
+  };
+  auto ask = [&](long long item) {
+    Move m = {0, 0, 0};
+    if (item < items) {
+      const long long i = item / parts;
+      m.src = ldg_cg_i32(a.moves + 2 * i);
+      m.dst = ldg_cg_i32(a.moves + 2 * i + 1);
+      m.tokens = a.tokens ? ldg_cg_i32(a.tokens + i) : a.block_size;
     }
-    int slots = a.block_size;
-    if (a.tokens) {
-      const int t = ldg_cg_i32(a.tokens + i);
-      if ((t < 0 || t > slots) && threadIdx.x == 0) attn_error(a.status);
-      slots = min(max(t, 0), slots);
+    return m;
+  };
+  Move next = ask(blockIdx.x);
+  for (long long item = blockIdx.x; item < items; item += gridDim.x) {
+    const Move m = next;
+    next = ask(item + gridDim.x);
+    const bool bad = m.src < 0 || m.src >= a.num_blocks || m.dst < 0 || m.dst >= a.num_blocks;
+    if ((bad || m.tokens < 0 || m.tokens > a.block_size) && threadIdx.x == 0) attn_error(a.status);
+    if (bad) continue;
+    const int end = min(max(m.tokens, 0), a.block_size) * a.nkv;  // rows to copy
+    int r = (int)(item % parts) * kCopyRows + (int)threadIdx.x / 16;
+    int slot = r / a.nkv, head = r - slot * a.nkv;
+    const long long src = m.src * a.s_block, to = m.dst * a.s_block - src;
+    long long at[kRowsPer];
+    uint4 kv[kRowsPer], vv[kRowsPer];
+#pragma unroll
+    for (int x = 0; x < kRowsPer; ++x) {
+      at[x] = r < end ? src + slot * a.s_slot + head * a.s_head + 8 * ((int)threadIdx.x % 16) : -1;
+      if (at[x] >= 0) {
+        kv[x] = ldg_cg_v4(a.k + at[x]);
+        vv[x] = ldg_cg_v4(a.v + at[x]);
+      }
+      r += kRowStep;
+      slot += step_slot;
+      head += step_head;
+      if (head >= a.nkv) {
+        head -= a.nkv;
+        ++slot;
+      }
     }
-    for (int r = threadIdx.x / 16; r < slots * a.nkv; r += kCopyThreads / 16) {
-      const long long at = (long long)(r / a.nkv) * a.s_slot + (long long)(r % a.nkv) * a.s_head + 8 * (threadIdx.x % 16);
-      const uint4 kv = ldg_cg_v4(a.k + src * a.s_block + at);
-      const uint4 vv = ldg_cg_v4(a.v + src * a.s_block + at);
-      *reinterpret_cast<uint4*>(a.k + dst * a.s_block + at) = kv;
-      *reinterpret_cast<uint4*>(a.v + dst * a.s_block + at) = vv;
-    }
+#pragma unroll
+    for (int x = 0; x < kRowsPer; ++x)
+      if (at[x] >= 0) {
+        *reinterpret_cast<uint4*>(a.k + at[x] + to) = kv[x];
+        *reinterpret_cast<uint4*>(a.v + at[x] + to) = vv[x];
+      }
   }
 }
 
-// Pages of sequence b (its length taken into the table's reach).
-FLINT_DEV int seq_pages(const KvPlanArgs& a, int b) {
-  const int n = ldg_cg_i32(a.seq_lens + b);
+// Pages of a sequence of n keys, n taken into the table's reach.
+FLINT_DEV int seq_pages(const KvPlanArgs& a, int n) {
   const long long most = (long long)a.max_blocks * a.block_size;
   if (n < 0 || n > most) {
     attn_error(a.status);
     return n < 0 ? 0 : a.max_blocks;
   }
   return (int)(((long long)n + a.block_size - 1) / a.block_size);
-}
-
-__global__ void __launch_bounds__(256) kv_mark_kernel(const KvPlanArgs a) {
-  SpanGuard<kSpanKvPlan> span_guard;
-  pdl_wait();
-  pdl_launch_dependents();
-  for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
-    const int used = seq_pages(a, b);
-    for (int i = threadIdx.x; i < used; i += 256) {
-      const int p = ldg_cg_i32(a.block_table + (long long)b * a.table_stride + i);
-      if (p < 0 || p >= a.num_blocks)
-        attn_error(a.status);
-      else
-        atomicOr(a.live + (p >> 5), 1u << (p & 31));
-    }
-  }
 }
 
 FLINT_DEV uint32_t ldg_cg_u32(const uint32_t* p) { return (uint32_t)ldg_cg_i32(reinterpret_cast<const int*>(p)); }
@@ -99,85 +121,105 @@ FLINT_DEV int scan_cta(int v, int* warps, int* all) {
   return r;
 }
 
-__global__ void __launch_bounds__(kPlanThreads) kv_rank_kernel(const KvPlanArgs a) {
+// The used pages' bits; then, in the CTA that comes last, the ranks and pairs.
+__global__ void __launch_bounds__(kPlanThreads) kv_mark_kernel(const KvPlanArgs a) {
   SpanGuard<kSpanKvPlan> span_guard;
   pdl_wait();
   pdl_launch_dependents();
   __shared__ int warps[32];
+  __shared__ int s_last;
+  for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
+    // (the first entries are asked for together with the length)
+    const int* row = a.block_table + (long long)b * a.table_stride;
+    int p = (int)threadIdx.x < a.max_blocks ? ldg_cg_i32(row + threadIdx.x) : 0;
+    const int used = seq_pages(a, ldg_cg_i32(a.seq_lens + b));
+    for (int i = threadIdx.x; i < used; i += kPlanThreads) {
+      if (i >= kPlanThreads) p = ldg_cg_i32(row + i);
+      if (p < 0 || p >= a.num_blocks)
+        attn_error(a.status);
+      else
+        atomicOr(a.live + (p >> 5), 1u << (p & 31));
+    }
+  }
+  __threadfence();
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    const int last = atomicAdd(a.done, 1) == (int)gridDim.x - 1;
+    if (last) *a.done = 0;
+    s_last = last;
+    __threadfence();
+  }
+  __syncthreads();
+  if (!s_last) return;
   const int words = (a.num_blocks + 31) / 32;
   int live = 0;
   for (int w0 = 0; w0 < words; w0 += kPlanThreads) {
     const int w = w0 + threadIdx.x;
+    const uint32_t bits = w < words ? ldg_cg_u32(a.live + w) : 0u;
     int all;
-    const int below = scan_cta(w < words ? __popc(ldg_cg_u32(a.live + w)) : 0, warps, &all);
-    if (w < words) a.rank[w] = live + below;
+    const int below = scan_cta(__popc(bits), warps, &all);
+    if (w < words) {
+      a.rank[w] = live + below;
+      a.bits[w] = bits;
+      a.live[w] = 0u;
+    }
     live += all;
   }
-  // `rank[w]` was written by this very thread
-  int above = 0;  // live pages at or above `live` = unused pages below it
-  for (int w0 = 0; w0 < words; w0 += kPlanThreads) {
-    const int w = w0 + threadIdx.x;
-    int c = 0;
-    if (w < words) {
-      const uint32_t bits = ldg_cg_u32(a.live + w);
-      const int p0 = 32 * w;
-      const uint32_t ge = p0 >= live ? ~0u : (live - p0 >= 32 ? 0u : ~0u << (live - p0));
-      c = __popc(bits & ge);
+  // live pages below `live`: what its word's rank and lower bits say
+  __shared__ int s_low;
+  if (threadIdx.x == 0) s_low = live;  // (all pages are live)
+  __syncthreads();
+  if (live < a.num_blocks && (live >> 5) % kPlanThreads == (int)threadIdx.x)  // the thread that wrote that word
+    s_low = a.rank[live >> 5] + __popc(a.bits[live >> 5] & ((1u << (live & 31)) - 1u));
+  __syncthreads();
+  const int low = s_low;
+  for (int w = threadIdx.x; w < words; w += kPlanThreads) {
+    const int p0 = 32 * w, rank = a.rank[w];
+    const uint32_t bits = a.bits[w];
+    const uint32_t ge = p0 >= live ? ~0u : (live - p0 >= 32 ? 0u : ~0u << (live - p0));
+    for (uint32_t x = bits & ge; x; x &= x - 1u) {  // used, to be moved
+      const int i = __ffs(x) - 1;
+      a.moves[2 * (long long)(rank + __popc(bits & ((1u << i) - 1u)) - low)] = p0 + i;
     }
-    int all;
-    scan_cta(c, warps, &all);
-    above += all;
-  }
-  const int low = live - above;  // live pages below `live`
-  for (int w0 = 0; w0 < words; w0 += kPlanThreads) {
-    const int w = w0 + threadIdx.x;
-    if (w >= words) continue;
-    const uint32_t bits = ldg_cg_u32(a.live + w);
-    int rank = a.rank[w];
-    for (int i = 0; i < 32 && 32 * w + i < a.num_blocks; ++i) {
-      const int p = 32 * w + i;
-      const bool on = (bits >> i) & 1u;
-      if (on && p >= live) a.moves[2 * (long long)(rank - low)] = p;
-      if (!on && p < live) a.moves[2 * (long long)(p - rank) + 1] = p;
-      rank += on;
+    for (uint32_t x = ~bits & ~ge; x; x &= x - 1u) {  // unused, to be filled
+      const int i = __ffs(x) - 1;
+      a.moves[2 * (long long)(p0 + i - rank - __popc(bits & ((1u << i) - 1u))) + 1] = p0 + i;
     }
   }
-  for (int i = 2 * above + threadIdx.x; i < a.num_blocks / 2 * 2; i += kPlanThreads) a.moves[i] = -1;
   if (threadIdx.x == 0) {
     a.counts[0] = live;
-    a.counts[1] = above;
+    a.counts[1] = live - low;
   }
 }
 
-__global__ void __launch_bounds__(256) kv_rename_kernel(const KvPlanArgs a) {
+constexpr int kRenameThreads = 512;
+__global__ void __launch_bounds__(kRenameThreads) kv_rename_kernel(const KvPlanArgs a) {
   SpanGuard<kSpanKvPlan> span_guard;
   pdl_wait();
   pdl_launch_dependents();
-  const int live = ldg_cg_i32(a.counts), low = live - ldg_cg_i32(a.counts + 1);
+  const int live = ldg_cg_i32(a.counts), above = ldg_cg_i32(a.counts + 1), low = live - above;
   for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
-    const int used = seq_pages(a, b);
-    for (int i = threadIdx.x; i < a.max_blocks; i += 256) {
+    const int* row = a.block_table + (long long)b * a.table_stride;
+    const int n = ldg_cg_i32(a.seq_lens + b);
+    int at = (int)threadIdx.x < a.max_blocks ? ldg_cg_i32(row + threadIdx.x) : 0;
+    const int used = seq_pages(a, n);
+    for (int i = threadIdx.x; i < a.max_blocks; i += kRenameThreads) {
       int p = -1;
       if (i < used) {
-        p = ldg_cg_i32(a.block_table + (long long)b * a.table_stride + i);
+        p = i < kRenameThreads ? at : ldg_cg_i32(row + i);
         if (p < 0 || p >= a.num_blocks) {
           p = -1;
         } else if (p >= live) {
-          const int rank = ldg_cg_i32(a.rank + (p >> 5)) + __popc(ldg_cg_u32(a.live + (p >> 5)) & ((1u << (p & 31)) - 1));
+          const int rank = ldg_cg_i32(a.rank + (p >> 5)) + __popc(ldg_cg_u32(a.bits + (p >> 5)) & ((1u << (p & 31)) - 1));
           p = ldg_cg_i32(a.moves + 2 * (long long)(rank - low) + 1);
         }
       }
       a.new_table[(long long)b * a.max_blocks + i] = p;
     }
   }
-}
-
-__global__ void __launch_bounds__(256) kv_clear_kernel(const KvPlanArgs a) {
-  SpanGuard<kSpanKvPlan> span_guard;
-  pdl_wait();
-  pdl_launch_dependents();
-  const int words = (a.num_blocks + 31) / 32;
-  for (int w = blockIdx.x * 256 + threadIdx.x; w < words; w += gridDim.x * 256) a.live[w] = 0;
+  const long long end = a.num_blocks / 2 * 2;  // (of the list's ints)
+  for (long long i = 2ll * above + blockIdx.x * kRenameThreads + threadIdx.x; i < end;
+       i += (long long)gridDim.x * kRenameThreads) a.moves[i] = -1;
 }
 
 template <class Args>
@@ -202,22 +244,21 @@ cudaError_t launch_kv_copy(const KvCopyArgs& a, cudaStream_t st) {
   int sms = 0;
   cudaError_t err = device_sms(&sms);
   if (err != cudaSuccess) return err;
-  const int grid = a.num_moves < 8 * sms ? a.num_moves : 8 * sms;
-  return launch_pdl(reinterpret_cast<const void*>(kv_copy_kernel), (unsigned)grid, kCopyThreads, a, st);
+  const long long parts = ((long long)a.block_size * a.nkv + kCopyRows - 1) / kCopyRows;
+  const long long items = a.num_moves * parts, most = 8ll * sms;
+  return launch_pdl(reinterpret_cast<const void*>(kv_copy_kernel), (unsigned)(items < most ? items : most),
+                    kCopyThreads, a, st);
 }
 
 cudaError_t launch_kv_plan(const KvPlanArgs& a, cudaStream_t st) {
   int sms = 0;
   cudaError_t err = device_sms(&sms);
   if (err != cudaSuccess) return err;
-  const unsigned rows = (unsigned)(a.B < 4 * sms ? (a.B < 1 ? 1 : a.B) : 4 * sms);
-  const int words = (a.num_blocks + 31) / 32;
-  const unsigned clear = (unsigned)((words + 255) / 256 < sms ? (words + 255) / 256 : sms);
-  err = launch_pdl(reinterpret_cast<const void*>(kv_mark_kernel), rows, 256, a, st);
-  if (err == cudaSuccess) err = launch_pdl(reinterpret_cast<const void*>(kv_rank_kernel), 1, kPlanThreads, a, st);
-  if (err == cudaSuccess) err = launch_pdl(reinterpret_cast<const void*>(kv_rename_kernel), rows, 256, a, st);
-  if (err == cudaSuccess) err = launch_pdl(reinterpret_cast<const void*>(kv_clear_kernel), clear, 256, a, st);
-  return err;
+  const int rows = a.B < 1 ? 1 : a.B;
+  err = launch_pdl(reinterpret_cast<const void*>(kv_mark_kernel), (unsigned)(rows < sms ? rows : sms), kPlanThreads, a, st);
+  if (err != cudaSuccess) return err;
+  return launch_pdl(reinterpret_cast<const void*>(kv_rename_kernel), (unsigned)(rows < 4 * sms ? rows : 4 * sms),
+                    kRenameThreads, a, st);
 }
 
 FLINT_SPAN_SETTER(kv_pages)
