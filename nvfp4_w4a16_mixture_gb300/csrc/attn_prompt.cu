@@ -15,21 +15,19 @@
 // it moves (and O and the sum are rescaled) only when some score exceeds it
 // by more than 8, so P stays below 2^8 and O is seldom touched.
 //
-// One CTA per SM, 12 warps, the third warpgroup leaving registers to the
+// One CTA per SM, 16 warps, the last two warpgroups leaving registers to the
 // softmax:
-//   warps 0-3, 4-7: softmax of row tile 0, 1 (thread = row): Q into swizzled
-//     shared memory, then per key tile S from TMEM, P back, and at the
-//     unit's end O to the output;
-//   warp 8: MMA issue.  Order S_0(0) S_1(0), then per j: PV_0(j) S_0(j+1)
-//     PV_1(j) S_1(j+1): while one tile's softmax runs, the other's products
-//     do;
-//   warps 9, 11: the key and the value tiles (a ring of five 32 KB stages, K_0
-//     V_0 K_1 V_1 ..) by 16-byte asynchronous copies, the pages looked up one
-//     key per lane.  Tiled bulk copies would need a box per page: at 16 slots a
-//     page 32 boxes for a pair of tiles, about 90 cycles each, 4,500 cycles in
-//     all where the products take 2,048; and page sizes and strides that no
-//     tensor map takes would need another path;
-//   warp 10: walks along the CTA's work and publishes it to the others.
+//   warps 0-3, 4-7: softmax of row tile 0, 1 (thread = row): per key tile S
+//     from TMEM, P back, and at the unit's end O to the output;
+//   warps 8, 9: MMA issue for row tile 0, 1, in turns.  Order S_0(0) S_1(0),
+//     then per j: PV_0(j) S_0(j+1) PV_1(j) S_1(j+1): while one tile's softmax
+//     runs, the other's products do;
+//   warps 10, 11, 14, 15: the key and value tiles (a ring of five 32 KB
+//     stages, K_0 V_0 K_1 V_1 ..) by tiled copies of a page's slots, or (tiny
+//     pages, strides that no tensor map takes) by 16-byte copies, which take
+//     the load-store unit's time from the barriers and cost 15 % more;
+//   warp 12: Q of the next unit; warp 13: walks along the CTA's work and
+//     publishes it to the others.
 // Shared memory: Q 2 x 32 KB, ring 5 x 32 KB.  TMEM: S_0, S_1, O_0, O_1, 128
 // columns each.
 //
@@ -58,10 +56,10 @@ constexpr int kStageBytes = 2 * kHalf;
 constexpr int kStages = 5;
 constexpr int kOffRing = 2 * kStageBytes;  // after Q_0, Q_1
 constexpr int kOffCtl = kOffRing + kStages * kStageBytes;
-// A warp runs on scheduler warp % 4; the one that issues the MMAs shares its
-// own with no other busy warp than the two of the softmax.
-constexpr int kWarpMma = 8, kWarpIdle = 12, kWarpQ = 14, kWarpWalk = 15;
-constexpr int kWarpLoad = 9;               // 9 .. 11, 13: K, V, K, V
+// A warp runs on scheduler warp % 4: each has two of the softmax's, the MMA
+// warps share theirs with warps that seldom run, the loading ones have the
+// other two.
+constexpr int kWarpMma = 8, kWarpQ = 12, kWarpWalk = 13;  // 8, 9: MMA; 10, 11, 14, 15: loads of K, V, K, V
 constexpr int kThreads = 512;              // four warpgroups
 // Registers per thread: 128 at launch (65536 / 512); the two softmax
 // warpgroups take what the others give up: 2 * 200 + 2 * 56 = 4 * 128.
@@ -69,7 +67,7 @@ constexpr int kRegsLaunch = 128, kRegsSoftmax = 200, kRegsOther = 56;
 static_assert(2 * kRegsSoftmax + 2 * kRegsOther <= 4 * kRegsLaunch, "setmaxnreg.inc would wait for ever");
 constexpr int kInfo = 8;                   // key-tile records in flight
 constexpr int kPieces = 4;                 // pieces published ahead
-constexpr int kPieceReaders = 14;          // 8 softmax warps, MMA, Q, 4 loading ones
+constexpr int kPieceReaders = 15;          // all warps but the walking one
 // Weights, in halves of a key tile's time (0.8 us): a unit's fixed part (Q,
 // first scores, output: about 5.5 us), and the least work worth a CTA of its
 // own (a unit below it is not cut: joining its parts would cost 3 us and more).
@@ -95,6 +93,7 @@ struct Piece {
 struct Ctl {
   uint64_t full[kStages], empty[kStages];
   uint64_t q_full[2], q_free[2], s_full[2], p_full[2][2], o_full[2], o_free[2], wg[2];
+  uint64_t turn[2];  // row tile t may issue
   uint64_t piece_full[kPieces], piece_empty[kPieces];
   uint32_t tmem;
   int abort;
@@ -665,108 +664,113 @@ FLINT_DEV bool elect() {
 }
 FLINT_DEV uint64_t with_low(uint64_t desc, uint32_t low) { return (desc & 0xffffffff00000000ull) | low; }
 
-FLINT_DEV void mma_role(const Args& p, Ctl& C, uint8_t* smem, uint32_t tmem_any) {
+// One warp per row tile, taking turns: while one issues its products (the
+// tensor core's queue is short, so that takes as long as they do), the other
+// waits for what its own need.  The turns also keep the tiles out of step, so
+// that one's softmax runs beside the other's products.
+FLINT_DEV void mma_role(const Args& p, Ctl& C, uint8_t* smem, uint32_t tmem_any, int t_any) {
   int* status = p.a.status;
   const uint32_t idS = tc::idesc_bf16(kTile, kTile), idO = idS | tc::kIdescBMajorN;
-  const uint32_t tmem = uniform(tmem_any);
+  const uint32_t t = uniform((uint32_t)t_any);
+  const uint32_t tS = uniform(tmem_any) + kTile * t, tO = tS + 2 * kTile;
   // descriptors of the ring's first stage; a stage adds kStageBytes / 16 to
   // the low word (shared addresses stay below 2^18, inside its 14-bit field)
   const uint64_t dk0 = tc::desc_sw128(smem + kOffRing), dv0 = tc::desc_sw128_mn(smem + kOffRing, kHalf);
-  const uint32_t q_low = uniform((uint32_t)tc::desc_sw128(smem));
+  const uint32_t q_low = uniform((uint32_t)tc::desc_sw128(smem)) + t * (kStageBytes >> 4);
   const uint32_t k_low = uniform((uint32_t)dk0), v_low = uniform((uint32_t)dv0);
-  uint32_t st = 0, ph = 0;                 // the next ring stage and its phase
-  uint32_t par_q = 0, par_p = 0, par_o = 0;  // parities by tile (bit t)
-  uint32_t had = 0;                        // tiles that have had a unit (bit t)
+  uint32_t st = 0, ph = 0;                  // the next ring stage and its phase
+  uint32_t n_unit = 0, n_p = 0, n_turn = 0;  // units, key tiles and turns so far
+  bool opened = false;                       // whether there has been a unit of two row tiles
   auto next_stage = [&]() {
     if (++st == kStages) {
       st = 0;
       ph ^= 1u;
     }
   };
-  // S_t = Q_t K^T, K in stage sk; whether it is Q_t's last use, and K's
-  auto issue_s = [&](int t, uint32_t sk, bool last_q, bool last_k) {
+  // S_t = Q_t K^T, K in stage sk; whether it is Q_t's last use
+  auto issue_s = [&](uint32_t sk, bool last) {
     if (elect()) {
       const uint32_t low = k_low + sk * (kStageBytes >> 4);
 #pragma unroll
       for (int kk = 0; kk < 8; ++kk) {
         const uint32_t o = (uint32_t)((kk >> 2) * (kHalf >> 4) + 2 * (kk & 3));
-        tc::mma_bf16(tmem + (uint32_t)(kTile * t), with_low(dk0, q_low + (uint32_t)(t * (kStageBytes >> 4)) + o),
-                     with_low(dk0, low + o), idS, kk > 0);
+        tc::mma_bf16(tS, with_low(dk0, q_low + o), with_low(dk0, low + o), idS, kk > 0);
       }
       bar_arrive(smem_addr(&C.s_full[t]));  // orders the tile's record before the softmax's reads
       bar_commit(smem_addr(&C.s_full[t]));
-      if (last_q) bar_commit(smem_addr(&C.q_free[t]));
-      if (last_k) bar_commit(smem_addr(&C.empty[sk]));
+      if (last) bar_commit(smem_addr(&C.q_free[t]));
+      bar_commit(smem_addr(&C.empty[sk]));
     }
     __syncwarp();
   };
   for (uint32_t n = 0; piece_ready(C, n, status); ++n) {
     const int nt = (int)uniform((uint32_t)(C.piece[n % kPieces].t1 - C.piece[n % kPieces].t0));
-    const int tiles = uniform((uint32_t)C.piece[n % kPieces].rows) > kTile ? 2 : 1;
+    const bool both = uniform((uint32_t)C.piece[n % kPieces].rows) > kTile;
     piece_done(C, n);
     if (nt == 0) continue;
+    if (t == 1 && !both) {  // the unit has one row tile: the ring goes on without this one
+      for (int i = 0; i < 2 * nt; ++i) {
+        if (!wait(smem_addr(&C.full[st]), ph, C, status)) return;
+        if (elect()) bar_arrive(smem_addr(&C.empty[st]));
+        __syncwarp();
+        next_stage();
+      }
+      continue;
+    }
+    auto my_turn = [&]() { return !both || wait(smem_addr(&C.turn[t]), n_turn++ & 1u, C, status); };
+    auto your_turn = [&]() {
+      if (both) {
+        if (elect()) bar_arrive(smem_addr(&C.turn[1 - t]));
+        __syncwarp();
+      }
+    };
     // ring order K_0 V_0 K_1 V_1 ..
     if (!wait(smem_addr(&C.full[st]), ph, C, status)) return;
-    const uint32_t first = uniform(st);
-#pragma unroll 1
-    for (int t = 0; t < tiles; ++t) {
-      if (!wait(smem_addr(&C.q_full[t]), (par_q >> t) & 1u, C, status)) return;
-      par_q ^= 1u << t;
-      tc::fence_after_sync();
-      issue_s(t, first, nt == 1, t + 1 == tiles);
-    }
+    if (!wait(smem_addr(&C.q_full[t]), n_unit & 1u, C, status)) return;
+    // (tile 0 opens a unit, once tile 1 has issued all of the last one: a turn
+    // handed over twice before it is taken would be lost)
+    if ((t == 1 || opened) && !my_turn()) return;
+    opened = opened || both;
+    tc::fence_after_sync();
+    issue_s(uniform(st), nt == 1);
+    your_turn();
     next_stage();
-    bool has_v = false, has_k = false;  // whether V_j, K_j+1 are known to be there
     for (int j = 0; j < nt; ++j) {
       const bool more = j + 1 < nt;
       const uint32_t sv = uniform(st);
-      if (!has_v && !wait(smem_addr(&C.full[sv]), ph, C, status)) return;
+      if (!wait(smem_addr(&C.full[sv]), ph, C, status)) return;
       next_stage();
       const uint32_t sk = uniform(st);
       if (more) {
-        if (!has_k && !wait(smem_addr(&C.full[sk]), ph, C, status)) return;
+        if (!wait(smem_addr(&C.full[sk]), ph, C, status)) return;
         next_stage();
       }
-      has_v = has_k = false;
-      // (unrolled: a straight run of code is what the instruction fetch keeps
-      // up with)
+      // O_t of the CTA's previous unit has been read
+      if (j == 0 && n_unit > 0 && !wait(smem_addr(&C.o_free[t]), (n_unit - 1) & 1u, C, status)) return;
+      if (!wait(smem_addr(&C.p_full[t][0]), n_p & 1u, C, status)) return;
+      if (!my_turn()) return;
 #pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        if (t == 0 || tiles == 2) {
-          if (j == 0) {  // O_t of the CTA's previous unit has been read
-            if ((had >> t) & 1u) {
-              if (!wait(smem_addr(&C.o_free[t]), (par_o >> t) & 1u, C, status)) return;
-              par_o ^= 1u << t;
-            }
-            had |= 1u << t;
+      for (int half = 0; half < 2; ++half) {  // keys 0 .. 63, 64 .. 127
+        if (half == 1 && !wait(smem_addr(&C.p_full[t][1]), n_p & 1u, C, status)) return;
+        tc::fence_after_sync();
+        if (elect()) {
+          const uint32_t low = v_low + sv * (kStageBytes >> 4);
+#pragma unroll
+          for (int kk = 4 * half; kk < 4 * half + 4; ++kk)
+            tc::mma_bf16_ta(tO, tS + (uint32_t)(8 * kk), with_low(dv0, low + (uint32_t)(kk * (2048 >> 4))), idO,
+                            j > 0 || kk > 0);
+          if (half == 1) {
+            bar_commit(smem_addr(&C.empty[sv]));
+            if (!more) bar_commit(smem_addr(&C.o_full[t]));
           }
-          const bool last = t + 1 == tiles;
-#pragma unroll
-          for (int half = 0; half < 2; ++half) {  // keys 0 .. 63, 64 .. 127
-            if (!wait(smem_addr(&C.p_full[t][half]), (par_p >> t) & 1u, C, status)) return;
-            tc::fence_after_sync();
-            if (elect()) {
-              const uint32_t low = v_low + sv * (kStageBytes >> 4);
-#pragma unroll
-              for (int kk = 4 * half; kk < 4 * half + 4; ++kk)
-                tc::mma_bf16_ta(tmem + (uint32_t)(2 * kTile + kTile * t), tmem + (uint32_t)(kTile * t + 8 * kk),
-                                with_low(dv0, low + (uint32_t)(kk * (2048 >> 4))), idO, j > 0 || kk > 0);
-              if (half == 1) {
-                if (last) bar_commit(smem_addr(&C.empty[sv]));
-                if (!more) bar_commit(smem_addr(&C.o_full[t]));
-              }
-            }
-            __syncwarp();
-            // while products run: is the next K there already?
-            if (t == 1 && half == 0 && j + 2 < nt)
-              has_k = is_over(smem_addr(&C.full[st + 1 == kStages ? 0 : st + 1]), st + 1 == kStages ? ph ^ 1u : ph);
-          }
-          par_p ^= 1u << t;
-          if (more) issue_s(t, sk, j + 2 == nt, last);
-          if (t == 0 && more) has_v = is_over(smem_addr(&C.full[st]), ph);  // the next V?
         }
+        __syncwarp();
       }
+      ++n_p;
+      if (more) issue_s(sk, j + 2 == nt);
+      your_turn();
     }
+    ++n_unit;
   }
 }
 
@@ -1003,7 +1007,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
       mbar_init(&C.full[i], 2);
-      mbar_init(&C.empty[i], 1);
+      mbar_init(&C.empty[i], 2);
     }
     for (int i = 0; i < kPieces; ++i) {
       mbar_init(&C.piece_full[i], 1);
@@ -1018,6 +1022,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&C.o_full[t], 1);
       mbar_init(&C.o_free[t], 4);
       mbar_init(&C.wg[t], 4);
+      mbar_init(&C.turn[t], 1);
     }
     C.abort = 0;
     fence_mbar_init();
@@ -1034,14 +1039,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     softmax_role<TILED>(p, C, smem, tmem, warp >> 2);
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
-    if (warp == kWarpMma)
-      mma_role(p, C, smem, tmem);
+    if (warp < kWarpMma + 2)
+      mma_role(p, C, smem, tmem, warp - kWarpMma);
     else if (warp == kWarpWalk)
       walk_role(p, C);
     else if (warp == kWarpQ)
       q_role(p, C, smem);
-    else if (warp != kWarpIdle) {
-      const int i = warp == kWarpLoad + 4 ? 3 : warp - kWarpLoad, kv = i & 1, part = i >> 1;
+    else {
+      const int kv = warp & 1, part = warp >> 2 & 1;  // 10, 11, 14, 15
       if (TILED)
         load_tiled_role(p, maps, C, smem, kv, part);
       else

@@ -321,6 +321,17 @@ def test_prompt(lens, qlens, nq, nkv, page):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("longest,nq,nkv", [(200, 16, 4), (70, 8, 2), (150, 8, 8)])
+def test_prompt_many_units_of_one_and_two_row_tiles(longest, nq, nkv):
+    """Hundreds of short prompts: many units on every CTA, with one or two row
+    tiles in any order, some of them shared."""
+    n = [(37 * i * i + 11 * i) % longest + 1 for i in range(300)]
+    p = Problem(n, n, nq, nkv, 16, seed=longest)
+    out, lse = run_prompt(p)
+    check(out, lse, p.expect(SCALE, P_BF16), f"many units {longest}")
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("layout", LAYOUTS)
 def test_prompt_layouts(layout):
     p = Problem([177, 300, 5], [177, 140, 5], 16, 4, 16, layout=layout, seed=5)
