@@ -216,84 +216,108 @@ FLINT_DEV long long scan_cta64(long long v, long long* warps, long long* all) {
   return r;
 }
 
-// One CTA: entries of all sequences, their weights' prefix sums, and the
-// first unit of each of the main kernel's CTAs.
+// One CTA: the entries of all sequences, their weights' prefix sums, and the
+// first unit of each of the main kernel's CTAs.  The sequences' data pass
+// through shared memory, kPlanThreads at a time; an entry finds its sequence
+// there by bisection.  Its weights are summed first (once more with a least
+// weight where there is little work), then everything is written.
 constexpr int kPlanThreads = 1024;
+struct PlanShared {
+  int lo[kPlanThreads], n[kPlanThreads], keys[kPlanThreads], first[kPlanThreads + 1];
+  long long scan[32];
+};
+
+// Sum of the weights; with WRITE also the entries, prefixes and starts.
+template <bool WRITE>
+FLINT_DEV long long plan_pass(const Args& p, PlanShared& S, bool loaded, int least, long long total, long long ctas) {
+  const AttnArgs& a = p.a;
+  const int tid = threadIdx.x, G = a.nq / a.nkv;
+  const long long most = (long long)a.T * G / kUnitRows + a.B;  // entries that the table holds
+  long long sum = 0, e_base = 0;
+  for (int b0 = 0; b0 < a.B; b0 += kPlanThreads) {
+    const int n_seq = min(kPlanThreads, a.B - b0);
+    if (!loaded) {
+      int lo = 0, n = 0, keys = 0;
+      if (tid < n_seq) {
+        keys = seq_keys(a, b0 + tid);
+        seq_rows(a, b0 + tid, lo, n);
+      }
+      long long all;
+      const long long at = scan_cta64(((long long)n * G + kUnitRows - 1) / kUnitRows, S.scan, &all);
+      S.lo[tid] = lo;
+      S.n[tid] = n;
+      S.keys[tid] = keys;
+      S.first[tid] = (int)at;
+      if (tid == 0) S.first[kPlanThreads] = (int)all;
+      __syncthreads();
+    }
+    // (overlapping pieces of a bad cu_q could outgrow the table: cut off there)
+    const long long here = min((long long)S.first[kPlanThreads], most - e_base);
+    if (here < S.first[kPlanThreads] && tid == 0) attn_error(a.status);
+    for (long long e0 = 0; e0 < here; e0 += kPlanThreads) {
+      const int e = (int)e0 + tid;
+      Entry x = {};
+      long long w = 0;
+      if (e < here) {
+        int i = 0;  // the last sequence whose first entry is at most e
+        for (int step = kPlanThreads / 2; step; step >>= 1)
+          if (i + step < n_seq && S.first[i + step] <= e) i += step;
+        x.b = b0 + i;
+        x.lo = S.lo[i];
+        x.n = S.n[i];
+        x.keys = S.keys[i];
+        x.r0 = (e - S.first[i]) * kUnitRows;
+        x.rows = min(kUnitRows, x.n * G - x.r0);
+        const int seen = max(0, min(x.keys, x.keys - x.n + (x.r0 + x.rows - 1) / G + 1));  // by its last row
+        x.tiles = (seen + kTile - 1) / kTile;
+        w = weight(x, least);
+      }
+      long long all;
+      const long long at = sum + scan_cta64(w * a.nkv, S.scan, &all);
+      sum += all;
+      if (WRITE && e < here) {
+        const long long i = e_base + e, end = at + w * a.nkv;
+        const int4 x0 = make_int4(x.b, x.lo, x.n, x.keys), x1 = make_int4(x.r0, x.rows, x.tiles, 0);
+        p.w.entries[2 * i] = x0;
+        p.w.entries[2 * i + 1] = x1;
+        p.w.prefix[i] = at;
+        // the CTAs whose pieces begin inside the entry
+        for (int c = at == 0 ? 0 : piece_of(at - 1, total, ctas) + 1; c < ctas; ++c) {
+          const long long pos = cut(c, total, ctas);
+          if (pos >= end) break;
+          const long long rem = cut(c + 1, total, ctas) - pos;
+          const uint32_t in = (uint32_t)(pos - at);  // (an entry's weight is below 2^31)
+          int4* s = p.w.starts + kStartWords * c;
+          s[0] = make_int4((int)i, (int)(in / (uint32_t)w), (int)(in % (uint32_t)w), (int)ctas);
+          s[1] = make_int4((int)total, (int)(total >> 32), (int)rem, (int)(rem >> 32));
+          s[2] = x0;
+          s[3] = x1;
+          s[4] = make_int4(least, 0, 0, 0);
+        }
+      }
+    }
+    e_base += here;
+    if (a.B > kPlanThreads) __syncthreads();  // before the next sequences take the place
+  }
+  return sum;
+}
+
 __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const Args p, int ctas) {
   SpanGuard<kSpanAttnPrompt> span_guard;
   pdl_wait();
   pdl_launch_dependents();
-  __shared__ long long warps[32];
-  const AttnArgs& a = p.a;
-  const int tid = threadIdx.x, G = a.nq / a.nkv;
-  long long n_entries = 0;
-  for (int b0 = 0; b0 < a.B; b0 += kPlanThreads) {
-    const int b = b0 + tid;
-    int lo = 0, n = 0;
-    if (b < a.B) seq_rows(a, b, lo, n);
-    long long all;
-    const long long mine = b < a.B ? ((long long)n * G + kUnitRows - 1) / kUnitRows : 0;
-    const long long at = n_entries + scan_cta64(mine, warps, &all);
-    if (b < a.B) p.w.first[b] = (int)at;
-    n_entries += all;
-  }
-  if (tid == 0) p.w.first[a.B] = (int)n_entries;
-  __syncthreads();
-  // a warp per sequence writes its entries (overlapping pieces of a bad cu_q
-  // could outgrow the table: cut off there)
-  const long long most = (long long)a.T * G / kUnitRows + a.B;
-  if (n_entries > most) {
-    if (tid == 0) attn_error(a.status);
-    n_entries = most;
-  }
-  for (int b = tid >> 5; b < a.B; b += kPlanThreads / 32) {
-    int lo, n;
-    seq_rows(a, b, lo, n);
-    const int keys = seq_keys(a, b);
-    const int e0 = ldg_cg_i32(p.w.first + b), e1 = min((long long)ldg_cg_i32(p.w.first + b + 1), n_entries);
-    for (int e = e0 + (tid & 31); e < e1; e += 32) {
-      const int r0 = (e - e0) * kUnitRows, rows = min(kUnitRows, n * G - r0);
-      const int seen = max(0, min(keys, keys - n + (r0 + rows - 1) / G + 1));  // by its last row
-      p.w.entries[2 * (long long)e] = make_int4(b, lo, n, keys);
-      p.w.entries[2 * (long long)e + 1] =
-          make_int4(r0, rows, (seen + kTile - 1) / kTile, 0);
-    }
-  }
-  __syncthreads();
-  long long total = 0;
+  __shared__ PlanShared S;
+  long long total = plan_pass<false>(p, S, false, 0, 0, 0);
+  const bool loaded = p.a.B <= kPlanThreads;
   int least = 0;
-  for (;;) {
-    total = 0;
-    for (long long e0 = 0; e0 < n_entries; e0 += kPlanThreads) {
-      const long long e = e0 + tid;
-      long long all;
-      const long long mine = e < n_entries ? (long long)weight(load_entry(p.w.entries + 2 * e), least) * a.nkv : 0;
-      const long long at = total + scan_cta64(mine, warps, &all);
-      if (e < n_entries) p.w.prefix[e] = at;
-      total += all;
-    }
-    if (least != 0 || total / ctas >= kLeastWeight) break;
+  if (total / ctas < kLeastWeight) {
     least = kLeastWeight;
+    total = plan_pass<false>(p, S, loaded, least, 0, 0);
   }
-  if (tid == 0) p.w.prefix[n_entries] = total;
-  __syncthreads();
   const long long n_cta = total == 0 ? 0 : max(1ll, min((long long)ctas, total / kLeastWeight));
-  if (tid < ctas && tid >= n_cta) p.w.starts[kStartWords * tid] = make_int4(0, 0, 0, 0);
-  // CTA c's piece begins at floor(c total / n_cta); entry e writes those inside it
-  for (long long e = tid; e < n_entries; e += kPlanThreads) {
-    const long long w = weight(load_entry(p.w.entries + 2 * e), least), at = p.w.prefix[e], end = at + w * a.nkv;
-    for (long long c = (at * n_cta + total - 1) / total; c < n_cta; ++c) {
-      const long long pos = c * total / n_cta;
-      if (pos >= end) break;
-      const long long rem = (c + 1) * total / n_cta - pos;
-      int4* s = p.w.starts + kStartWords * c;
-      s[0] = make_int4((int)e, (int)((pos - at) / w), (int)((pos - at) % w), (int)n_cta);
-      s[1] = make_int4((int)total, (int)(total >> 32), (int)rem, (int)(rem >> 32));
-      s[2] = p.w.entries[2 * e];
-      s[3] = p.w.entries[2 * e + 1];
-      s[4] = make_int4(least, 0, 0, 0);
-    }
-  }
+  if ((int)threadIdx.x < ctas && (int)threadIdx.x >= n_cta)
+    p.w.starts[kStartWords * threadIdx.x] = make_int4(0, 0, 0, 0);
+  if (total != 0) plan_pass<true>(p, S, loaded, least, total, n_cta);
 }
 
 // ------------------------------------------------------------- the pieces
@@ -332,10 +356,10 @@ FLINT_DEV void walk_role(const Args& p, Ctl& C) {
       x.t1 = min((off + take) / kTileWeight, e.tiles);
       x.c_first = x.c_last = cta;
       x.valid = 1;
-      if (off > 0 || take < real) {  // CTA of position y: floor(((y + 1) ctas - 1) / total)
+      if (off > 0 || take < real) {
         const long long at = __ldcg(p.w.prefix + i) + (long long)h * w;
-        x.c_first = (int)(((at + 1) * ctas - 1) / total);
-        x.c_last = (int)(((at + real) * ctas - 1) / total);
+        x.c_first = piece_of(at, total, ctas);
+        x.c_last = piece_of(at + real - 1, total, ctas);
       }
       if (!publish(x)) return;
     }
@@ -369,13 +393,25 @@ FLINT_DEV uint32_t pack2(float a, float b) {
   return *reinterpret_cast<uint32_t*>(&r);
 }
 
-// A finished row's 32 columns from c0 on, scaled, to bf16.
+// 32 of a finished row's columns, scaled, to bf16.  Each lane writes a row of
+// its own, so a store takes as many cycles as it has lanes; 32 bytes a lane
+// where the output's alignment allows.
 FLINT_DEV void store_cols(uint16_t* dst, const float* o, float inv) {
+  uint32_t w[16];
 #pragma unroll
-  for (int i = 0; i < 32; i += 8)
-    *reinterpret_cast<uint4*>(dst + i) =
-        make_uint4(pack2(o[i] * inv, o[i + 1] * inv), pack2(o[i + 2] * inv, o[i + 3] * inv),
-                   pack2(o[i + 4] * inv, o[i + 5] * inv), pack2(o[i + 6] * inv, o[i + 7] * inv));
+  for (int i = 0; i < 16; ++i) w[i] = pack2(o[2 * i] * inv, o[2 * i + 1] * inv);
+  if ((reinterpret_cast<uintptr_t>(dst) & 31u) == 0) {
+#pragma unroll
+    for (int i = 0; i < 16; i += 8)
+      asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst + 2 * i), "r"(w[i]),
+                   "r"(w[i + 1]), "r"(w[i + 2]), "r"(w[i + 3]), "r"(w[i + 4]), "r"(w[i + 5]), "r"(w[i + 6]),
+                   "r"(w[i + 7])
+                   : "memory");
+  } else {
+#pragma unroll
+    for (int i = 0; i < 16; i += 4)
+      *reinterpret_cast<uint4*>(dst + 2 * i) = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
+  }
 }
 
 // -------------------------------------------------------------- the softmax
@@ -487,12 +523,6 @@ FLINT_DEV void softmax_role(const Args& p, Ctl& C, uint8_t* smem, uint32_t tmem,
         tc::tmem_wait_ld();
 #pragma unroll
         for (int i = 0; i < 4; ++i) tc::tmem_regs_ready(s[i]);
-        if (keys < kTile || lim0 < kTile - 1) {
-          const int vis = min(keys, lim + 1);
-#pragma unroll
-          for (int i = 0; i < kTile; ++i)
-            if (i >= vis) s[i >> 5][i & 31] = 0xff800000u;
-        }
         if (TILED && (keys < kTile || bad)) {
           // V's rows past the sequence's end or not loaded: zeros, whatever the
           // slots hold (P is 0 there).  V_j is in ring slot 2 n_tile + 1
@@ -505,46 +535,31 @@ FLINT_DEV void softmax_role(const Args& p, Ctl& C, uint8_t* smem, uint32_t tmem,
           }
           fence_proxy_async_smem();
         }
-        if (bad) {
+        if (keys < kTile || lim0 < kTile - 1 || bad) {
+          const int vis = min(keys, lim + 1);
 #pragma unroll
-          for (int i = 0; i < kTile; ++i)
-            if ((info.bad[i >> 5] >> (i & 31)) & 1u) s[i >> 5][i & 31] = 0xff800000u;
+          for (int i = 0; i < 4; ++i) {
+            const int left = vis - 32 * i;  // visible keys from the 32 on
+            uint32_t w = left >= 32 ? ~0u : (left <= 0 ? 0u : (1u << left) - 1u);
+            if (bad) w &= ~info.bad[i];
+#pragma unroll
+            for (int x = 0; x < 32; ++x)
+              if (!(w & (1u << x))) s[i][x] = 0xff800000u;
+          }
         }
-        // P of the first 64 keys against the reference so far, and beside it
-        // (other units of the SM) the tile's maximum
         float mx[4] = {neg_inf(), neg_inf(), neg_inf(), neg_inf()};
-        uint32_t pk[32];
-        unsigned long long sum[2] = {0ull, 0ull};
-        const unsigned long long c2 = pair(c, c);
-        auto exps = [&](int i, int x, uint32_t& out, unsigned long long neg2) {  // keys 32 i + x, + 1
-          float e0, e1;
-          unpair(fma2(pair(__uint_as_float(s[i][x]), __uint_as_float(s[i][x + 1])), c2, neg2), e0, e1);
-          e0 = ex2(e0);
-          e1 = ex2(e1);
-          sum[(x >> 1) & 1] = add2(sum[(x >> 1) & 1], pair(e0, e1));
-          out = pack2(e0, e1);
-        };
-        auto reference = [&]() {
-          const float neg = m == neg_inf() ? 0.0f : -m;
-          return pair(neg, neg);
-        };
-        unsigned long long neg2 = reference();
 #pragma unroll
-        for (int x = 0; x < 32; x += 2) {
-#pragma unroll
-          for (int i = 0; i < 2; ++i) exps(i, x, pk[16 * i + (x >> 1)], neg2);
+        for (int x = 0; x < 32; x += 2)
 #pragma unroll
           for (int i = 0; i < 4; ++i) mx[i] = max3(mx[i], __uint_as_float(s[i][x]), __uint_as_float(s[i][x + 1]));
-        }
         const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
         if (__any_sync(0xffffffffu, mt > m + kLazy)) {
-          // the reference moves: the first tile, and now and then later.  S(j)
-          // was issued after PV(j - 1) and has completed, so O is stable
+          // the reference moves: at the first tile, and now and then later
           const float to = fmaxf(m, mt);
-          const float r = m == to ? 1.0f : ex2(m - to);
-          m = to;
-          l *= r;
           if (j > 0) {
+            // S(j) was issued after PV(j - 1) and has completed, so O is stable
+            const float r = m == to ? 1.0f : ex2(m - to);
+            l *= r;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
               uint32_t o[16];
@@ -556,31 +571,33 @@ FLINT_DEV void softmax_role(const Args& p, Ctl& C, uint8_t* smem, uint32_t tmem,
               tc::tmem_st16(tO + 16 * i, o);
             }
           }
-          neg2 = reference();
-          sum[0] = sum[1] = 0ull;
-#pragma unroll
-          for (int i = 0; i < 2; ++i)
-#pragma unroll
-            for (int x = 0; x < 32; x += 2) exps(i, x, pk[16 * i + (x >> 1)], neg2);
+          m = to;
         }
+        const float neg = m == neg_inf() ? 0.0f : -m;
+        const unsigned long long c2 = pair(c, c), neg2 = pair(neg, neg);
+        unsigned long long sum[2] = {0ull, 0ull};
         // P over S's first columns; its product starts on the first 64 keys
         // while the rest follow
-        auto hand_over = [&](int half) {
-          tc::tmem_wait_st();
-          tc::fence_before_sync();
-          __syncwarp();
-          if (lane == 0) bar_arrive(smem_addr(&C.p_full[t][half]));
-        };
-        tc::tmem_st16(tS, pk);
-        tc::tmem_st16(tS + 16, pk + 16);
-        hand_over(0);
 #pragma unroll
-        for (int i = 2; i < 4; ++i) {
+        for (int i = 0; i < 4; ++i) {
+          uint32_t pk[16];
 #pragma unroll
-          for (int x = 0; x < 32; x += 2) exps(i, x, pk[x >> 1], neg2);
+          for (int x = 0; x < 32; x += 2) {
+            float e0, e1;
+            unpair(fma2(pair(__uint_as_float(s[i][x]), __uint_as_float(s[i][x + 1])), c2, neg2), e0, e1);
+            e0 = ex2(e0);
+            e1 = ex2(e1);
+            sum[(x >> 1) & 1] = add2(sum[(x >> 1) & 1], pair(e0, e1));
+            pk[x >> 1] = pack2(e0, e1);
+          }
           tc::tmem_st16(tS + 16 * i, pk);
+          if (i & 1) {
+            tc::tmem_wait_st();
+            tc::fence_before_sync();
+            __syncwarp();
+            if (lane == 0) bar_arrive(smem_addr(&C.p_full[t][i >> 1]));
+          }
         }
-        hand_over(1);
         float s0, s1;
         unpair(add2(sum[0], sum[1]), s0, s1);
         l += s0 + s1;
@@ -833,33 +850,44 @@ FLINT_DEV void load_tiled_role(const Args& p, const Maps& maps, Ctl& C, uint8_t*
   uint32_t st = (uint32_t)kv, ph = 0, uses = 0;
   int n_tile = 0;
   bool used = false, ok = true;
+  // Page (as the table has it; kNone where the tile has no such key) and slot
+  // of this lane's box; asked for a tile ahead, over the pieces.
+  constexpr int kNone = -0x7fffffff - 1;
+  auto look_up = [&](const Piece& u, int j, int& page, int& slot) {
+    const int pos = j * kTile + (lane << p.box_log2);
+    page = kNone;
+    if (lane < boxes && pos < u.keys) {
+      const int blk = pos / a.block_size;
+      slot = pos - blk * a.block_size;
+      page = ldg_cg_i32(a.block_table + (long long)u.b * a.table_stride + blk);
+    }
+  };
+  int next_page = kNone, next_slot = 0;
+  bool ahead = false;  // whether they are those of the coming piece's first tile
   for (uint32_t n = 0; ok && piece_ready(C, n, a.status); ++n) {
-    const Piece& u = C.piece[n % kPieces];
-    const int b = u.b, h = u.h, keys_all = u.keys, t0 = u.t0, t1 = u.t1;
+    const Piece u = C.piece[n % kPieces];
+    const int h = u.h, keys_all = u.keys, t0 = u.t0, t1 = u.t1;
     piece_done(C, n);
-    // page and slot of this lane's box of the tile at key0; page -1 outside the
-    // cache, -2 where the tile has no such key
-    auto look_up = [&](int key0, int& page, int& slot) {
-      const int pos = key0 + (lane << p.box_log2);
-      page = -2;
-      if (lane < boxes && pos < keys_all) {
-        const int blk = pos / a.block_size;
-        slot = pos - blk * a.block_size;
-        page = ldg_cg_i32(a.block_table + (long long)b * a.table_stride + blk);
-        if (page < 0 || page >= a.num_blocks) {
-          attn_error(a.status);
-          page = -1;
+    if (t0 < t1 && !ahead) look_up(u, t0, next_page, next_slot);
+    ahead = ahead && t0 >= t1;
+    for (int j = t0; j < t1; ++j, ++n_tile) {
+      const int raw = next_page, slot = next_slot;
+      if (j + 1 < t1) {
+        look_up(u, j + 1, next_page, next_slot);
+      } else if (is_over(smem_addr(&C.piece_full[(n + 1) % kPieces]), ((n + 1) / kPieces) & 1)) {
+        const Piece& v = C.piece[(n + 1) % kPieces];
+        if (v.valid && v.t0 < v.t1) {
+          look_up(v, v.t0, next_page, next_slot);
+          ahead = true;
         }
       }
-    };
-    int page = -2, slot = 0, next_page = -2, next_slot = 0;
-    if (t0 < t1) look_up(t0 * kTile, page, slot);
-    for (int j = t0; j < t1; ++j, ++n_tile) {
-      if (j + 1 < t1) look_up((j + 1) * kTile, next_page, next_slot);
       if (used && !wait(smem_addr(&C.empty[st]), ph ^ 1u, C, a.status)) {
         ok = false;
         break;
       }
+      const bool inside = raw >= 0 && raw < a.num_blocks;
+      if (!inside && raw != kNone) attn_error(a.status);
+      const int page = inside ? raw : (raw == kNone ? -2 : -1);
       const uint32_t good = __ballot_sync(0xffffffffu, page >= 0), bad = __ballot_sync(0xffffffffu, page == -1);
       if (kv == 0 && half == 0) {
         TileInfo& info = C.info[n_tile % kInfo];
@@ -889,8 +917,6 @@ FLINT_DEV void load_tiled_role(const Args& p, const Maps& maps, Ctl& C, uint8_t*
         used = true;
         ph ^= 1u;
       }
-      page = next_page;
-      slot = next_slot;
     }
   }
   if (aborted(C)) {  // no copy may land after the block has exited
@@ -1098,9 +1124,8 @@ PromptWs prompt_ws(void* base, int T, int B, int nq, int nkv) {
   w.count = reinterpret_cast<int*>(b + kAttnPromptCounters);
   w.parts = reinterpret_cast<float*>(take((size_t)2 * kPromptCtas * kPartFloats * sizeof(float)));
   w.starts = reinterpret_cast<int4*>(take(kPromptCtas * kStartWords * sizeof(int4)));
-  w.first = reinterpret_cast<int*>(take((size_t)(B + 1) * sizeof(int)));
   w.entries = reinterpret_cast<int4*>(take(entries * 2 * sizeof(int4)));
-  w.prefix = reinterpret_cast<long long*>(take((entries + 1) * sizeof(long long)));
+  w.prefix = reinterpret_cast<long long*>(take(entries * sizeof(long long)));
   w.total = off;
   return w;
 }

@@ -90,17 +90,6 @@ struct Part {
   int c_first, c_last;  // CTAs that share the unit
 };
 
-// The line of `total` weights is cut into n pieces (n <= 152): piece c begins
-// at floor(c total / n), position x lies in piece floor(((x + 1) n - 1) /
-// total).  32-bit arithmetic where it fits (a 64-bit division takes 0.3 us).
-FLINT_DEV long long cut(long long c, long long total, long long n) {
-  return total < (1 << 23) ? (long long)((uint32_t)c * (uint32_t)total / (uint32_t)n) : c * total / n;
-}
-FLINT_DEV int piece_of(long long x, long long total, long long n) {
-  return total < (1 << 23) ? (int)((((uint32_t)x + 1u) * (uint32_t)n - 1u) / (uint32_t)total)
-                           : (int)(((x + 1) * n - 1) / total);
-}
-
 // A walk along the CTA's piece of the line.
 template <int NT>
 struct Walk {

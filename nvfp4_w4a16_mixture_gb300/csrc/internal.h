@@ -263,9 +263,8 @@ constexpr int kPromptCtas = 152;  // most CTAs of its grid (one per SM)
 struct PromptWs {
   int* count;            // [2 * kPromptCtas]: finished parts of a shared unit, zero between calls
   int4* starts;          // [kPromptCtas, 5]: where each CTA's piece begins
-  int* first;            // [B + 1]: first entry of each sequence
   int4* entries;         // [entries, 2]
-  long long* prefix;     // [entries + 1]: weight before each entry
+  long long* prefix;     // [entries]: weight before each entry
   float* parts;          // [2 * kPromptCtas] slots
   size_t total;
 };
