@@ -44,4 +44,17 @@ bool attn_map(CUtensorMap* m, const AttnArgs& a, const uint16_t* base, int box) 
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool attn_q_map(CUtensorMap* m, const AttnArgs& a, int heads, int tokens) {
+  auto fn = encoder();
+  if (!fn) return false;
+  const cuuint64_t dims[3] = {128, (cuuint64_t)a.nq, (cuuint64_t)a.T};
+  const cuuint64_t strides[2] = {256, (cuuint64_t)(a.T > 1 ? a.q_stride * 2 : 256)};
+  if (strides[1] == 0 || strides[1] >= (1ull << 40)) return false;
+  const cuuint32_t bx[3] = {64, (cuuint32_t)heads, (cuuint32_t)tokens};
+  const cuuint32_t es[3] = {1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<uint16_t*>(a.q), dims, strides, bx, es,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 }  // namespace flint

@@ -156,9 +156,11 @@ struct Args {
   AttnArgs a;
   PromptWs w;
   int box, box_log2;  // rows of a tiled copy: gcd(block_size, 128)
+  int q_tiled;        // whether maps.q is there
 };
 struct Maps {
   CUtensorMap k, v;  // {128, heads, slots, pages}, box {64, 1, box, 1}
+  CUtensorMap q;     // {128, heads, T}, box {64, G, 128 / G}
 };
 
 // ---------------------------------------------------------------- the plan
@@ -792,9 +794,10 @@ FLINT_DEV void mma_role(const Args& p, Ctl& C, uint8_t* smem, uint32_t tmem_any,
 }
 
 // ------------------------------------------------------------------ the loads
-// Q's rows, 16 lanes per row, each row tile as soon as the last product with
-// the previous unit's is done.
-FLINT_DEV void q_role(const Args& p, Ctl& C, uint8_t* smem) {
+// Q's rows, each row tile as soon as the last product with the previous
+// unit's is done: two tiled copies where G divides the tile (its rows are then
+// whole tokens), else 16-byte copies, 16 lanes per row.
+FLINT_DEV void q_role(const Args& p, const Maps& maps, Ctl& C, uint8_t* smem) {
   const AttnArgs& a = p.a;
   const int lane = threadIdx.x & 31, hi = lane >> 4, ch = lane & 15, G = a.nq / a.nkv;
   uint32_t to[4];
@@ -805,17 +808,27 @@ FLINT_DEV void q_role(const Args& p, Ctl& C, uint8_t* smem) {
   uint32_t used[2] = {0, 0};
   for (uint32_t n = 0; piece_ready(C, n, a.status); ++n) {
     const Piece& u = C.piece[n % kPieces];
-    const int rows = u.rows, nt = u.t1 - u.t0;
-    const int q = u.r0 + hi, token = q / G;
-    int head = q - token * G;
-    const uint16_t* from = a.q + (long long)(u.lo + token) * a.q_stride + (long long)(u.h * G + head) * kHeadDim + 8 * ch;
+    const int rows = u.rows, nt = u.t1 - u.t0, h = u.h, lo = u.lo, r0 = u.r0;
     piece_done(C, n);
     if (nt == 0) continue;
-#pragma unroll
+#pragma unroll 1
     for (int t = 0; t < 2; ++t) {
       if (rows <= kTile * t) break;
-      if (used[t] > 0 && !wait(smem_addr(&C.q_free[t]), (used[t] - 1) & 1, C, a.status)) return;
+      if (used[t] > 0 && !wait(smem_addr(&C.q_free[t]), (used[t] - 1) & 1, C, a.status)) break;
       ++used[t];
+      if (p.q_tiled) {  // (rows past the unit's are other tokens', or zeros past T)
+        if (lane == 0) {
+          bar_expect(smem_addr(&C.q_full[t]), kStageBytes);
+          for (int half = 0; half < 2; ++half)
+            tc::tma_load_3d(smem + t * kStageBytes + half * kHalf, &maps.q, 64 * half, h * G, lo + (r0 + kTile * t) / G,
+                            &C.q_full[t]);
+        }
+        __syncwarp();
+        continue;
+      }
+      const int q = r0 + kTile * t + hi, token = q / G;
+      int head = q - token * G;
+      const uint16_t* from = a.q + (long long)(lo + token) * a.q_stride + (long long)(h * G + head) * kHeadDim + 8 * ch;
       for (int i0 = 0; i0 < 64; i0 += 4) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -834,6 +847,13 @@ FLINT_DEV void q_role(const Args& p, Ctl& C, uint8_t* smem) {
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) bar_arrive(smem_addr(&C.q_full[t]));
+    }
+  }
+  if (p.q_tiled && aborted(C)) {  // no copy may land after the block has exited
+    for (int t = 0; t < 2; ++t) {
+      const uint32_t t0 = globaltimer_low();
+      while (used[t] > 0 && !bar_test(smem_addr(&C.q_full[t]), (used[t] - 1) & 1) && globaltimer_low() - t0 < kWaitNs) {
+      }
     }
   }
 }
@@ -1070,7 +1090,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     else if (warp == kWarpWalk)
       walk_role(p, C);
     else if (warp == kWarpQ)
-      q_role(p, C, smem);
+      q_role(p, maps, C, smem);
     else {
       const int kv = warp & 1, part = warp >> 2 & 1;  // 10, 11, 14, 15
       if (TILED)
@@ -1138,6 +1158,8 @@ cudaError_t launch_attn_prompt(const AttnArgs& a, const PromptWs& w, cudaStream_
   for (p.box_log2 = 0; (1 << p.box_log2) < p.box;) ++p.box_log2;
   Maps maps = {};
   const bool tiled = p.box >= kAttnMinBox && attn_map(&maps.k, a, a.k, p.box) && attn_map(&maps.v, a, a.v, p.box);
+  const int G = a.nq / a.nkv;
+  p.q_tiled = kTile % G == 0 && attn_q_map(&maps.q, a, G, kTile / G);
   int sms = 0;
   cudaError_t err = device_sms(&sms);
   if (err != cudaSuccess) return err;

@@ -242,6 +242,9 @@ int attn_box(int block_size, int most);
 // 128-byte swizzle; false for strides that no tensor map takes.
 bool attn_map(CUtensorMap* m, const AttnArgs& a, const uint16_t* base, int box);
 
+// The map {128 dims, heads, T} of the queries with boxes of {64, heads, tokens}.
+bool attn_q_map(CUtensorMap* m, const AttnArgs& a, int heads, int tokens);
+
 // Workspaces of both attention kernels: the status word, each kernel's
 // counters (zero between calls) at a place of its own, then data.
 constexpr size_t kAttnRowsCounters = 256, kAttnPromptCounters = 1024, kAttnData = 4096;
