@@ -3,8 +3,8 @@
 //
 // Rows: as in attn_rows.cu, packed row r of a sequence and kv head is token
 // r / G, head r % G, so the keys are loaded once for the G query heads of a
-// group and a causal border crosses few tokens.  A unit is up to 256 packed
-// rows (two tiles of 128) of one (sequence, kv head) and the 128-key tiles
+// group and a causal border crosses few tokens.  A unit is up to two row tiles
+// of 128 (whole tokens: 126 rows for G = 7) of one (sequence, kv head) and the 128-key tiles
 // that they see.
 //
 // Per key tile j and row tile t: S_t = Q_t K_j^T (128 x 128, fp32 in TMEM),
@@ -50,7 +50,7 @@ namespace flint {
 namespace {
 
 constexpr int kTile = 128;                 // rows of a row tile; keys of a key tile
-constexpr int kUnitRows = 2 * kTile;
+constexpr int kUnitSlots = 2 * kTile;      // rows of a unit's parts in the workspace
 constexpr int kHalf = kTile * 128;         // 128 rows x 64 bf16
 constexpr int kStageBytes = 2 * kHalf;
 constexpr int kStages = 5;
@@ -75,7 +75,11 @@ constexpr int kTileWeight = 2, kUnitWeight = 7, kLeastWeight = 24;
 constexpr float kLazy = 8.0f;
 constexpr uint32_t kWaitNs = 200u * 1000 * 1000;
 constexpr uint32_t kSuspendNs = 50000;
-constexpr int kPartFloats = kUnitRows * (kHeadDim + 2);
+constexpr int kPartFloats = kUnitSlots * (kHeadDim + 2);
+
+// Rows of a row tile that are used: whole tokens where a token's group fits
+// (Q's tiled copies start at a token), all of them otherwise.
+__host__ __device__ constexpr int tile_rows(int G) { return G <= kTile ? kTile / G * G : kTile; }
 
 struct TileInfo {
   int keys;         // valid keys of the tile (from its start)
@@ -156,11 +160,12 @@ struct Args {
   AttnArgs a;
   PromptWs w;
   int box, box_log2;  // rows of a tiled copy: gcd(block_size, 128)
+  int tile_rows;      // rows of a row tile
   int q_tiled;        // whether maps.q is there
 };
 struct Maps {
   CUtensorMap k, v;  // {128, heads, slots, pages}, box {64, 1, box, 1}
-  CUtensorMap q;     // {128, heads, T}, box {64, G, 128 / G}
+  CUtensorMap q;     // {128, heads, T}, box {64, G, tile_rows / G}
 };
 
 // ---------------------------------------------------------------- the plan
@@ -234,7 +239,8 @@ template <bool WRITE>
 FLINT_DEV long long plan_pass(const Args& p, PlanShared& S, bool loaded, int least, long long total, long long ctas) {
   const AttnArgs& a = p.a;
   const int tid = threadIdx.x, G = a.nq / a.nkv;
-  const long long most = (long long)a.T * G / kUnitRows + a.B;  // entries that the table holds
+  const int unit_rows = 2 * p.tile_rows;
+  const long long most = (long long)a.T * G / unit_rows + a.B;  // entries that the table holds
   long long sum = 0, e_base = 0;
   for (int b0 = 0; b0 < a.B; b0 += kPlanThreads) {
     const int n_seq = min(kPlanThreads, a.B - b0);
@@ -245,7 +251,7 @@ FLINT_DEV long long plan_pass(const Args& p, PlanShared& S, bool loaded, int lea
         seq_rows(a, b0 + tid, lo, n);
       }
       long long all;
-      const long long at = scan_cta64(((long long)n * G + kUnitRows - 1) / kUnitRows, S.scan, &all);
+      const long long at = scan_cta64(((long long)n * G + unit_rows - 1) / unit_rows, S.scan, &all);
       S.lo[tid] = lo;
       S.n[tid] = n;
       S.keys[tid] = keys;
@@ -268,8 +274,8 @@ FLINT_DEV long long plan_pass(const Args& p, PlanShared& S, bool loaded, int lea
         x.lo = S.lo[i];
         x.n = S.n[i];
         x.keys = S.keys[i];
-        x.r0 = (e - S.first[i]) * kUnitRows;
-        x.rows = min(kUnitRows, x.n * G - x.r0);
+        x.r0 = (e - S.first[i]) * unit_rows;
+        x.rows = min(unit_rows, x.n * G - x.r0);
         const int seen = max(0, min(x.keys, x.keys - x.n + (x.r0 + x.rows - 1) / G + 1));  // by its last row
         x.tiles = (seen + kTile - 1) / kTile;
         w = weight(x, least);
@@ -454,10 +460,11 @@ FLINT_DEV float* part_of(const Args& p, const Piece& u, int cta) {
   return p.w.parts + (size_t)(2 * cta + (cta == u.c_first)) * kPartFloats;
 }
 
-// The parts of a shared unit, joined in CTA order, for packed row R.
-FLINT_DEV void join_row(const Args& p, const Piece& u, int R) {
+// The parts of a shared unit, joined in CTA order, for the row in slot `at`,
+// packed row R (if it is one of the unit's).
+FLINT_DEV void join_row(const Args& p, const Piece& u, int at, int R, bool valid) {
   float m = neg_inf();
-  for (int x = u.c_first; x <= u.c_last; ++x) m = fmaxf(m, __ldcg(part_of(p, u, x) + kHeadDim * kUnitRows + R));
+  for (int x = u.c_first; x <= u.c_last; ++x) m = fmaxf(m, __ldcg(part_of(p, u, x) + kHeadDim * kUnitSlots + at));
   float l = 0.0f;
   float o[4][32];
 #pragma unroll
@@ -466,19 +473,19 @@ FLINT_DEV void join_row(const Args& p, const Piece& u, int R) {
     for (int x = 0; x < 32; ++x) o[i][x] = 0.0f;
   for (int x = u.c_first; x <= u.c_last; ++x) {
     const float* pp = part_of(p, u, x);
-    const float pm = __ldcg(pp + kHeadDim * kUnitRows + R), pl = __ldcg(pp + (kHeadDim + 1) * kUnitRows + R);
+    const float pm = __ldcg(pp + kHeadDim * kUnitSlots + at), pl = __ldcg(pp + (kHeadDim + 1) * kUnitSlots + at);
     const float f = pm == neg_inf() ? (pl == 0.0f ? 0.0f : 1.0f) : ex2(pm - m);
     l += f * pl;
 #pragma unroll
     for (int i = 0; i < 32; ++i) {
-      const float4 v = __ldcg(reinterpret_cast<const float4*>(pp) + (size_t)i * kUnitRows + R);
+      const float4 v = __ldcg(reinterpret_cast<const float4*>(pp) + (size_t)i * kUnitSlots + at);
       o[i >> 3][4 * (i & 7)] += f * v.x;
       o[i >> 3][4 * (i & 7) + 1] += f * v.y;
       o[i >> 3][4 * (i & 7) + 2] += f * v.z;
       o[i >> 3][4 * (i & 7) + 3] += f * v.w;
     }
   }
-  if (R < u.rows) {
+  if (valid) {
     const long long row = out_row(p.a, u, R);
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;
 #pragma unroll
@@ -491,7 +498,8 @@ template <bool TILED>
 FLINT_DEV void softmax_role(const Args& p, Ctl& C, uint8_t* smem, uint32_t tmem, int t) {
   const AttnArgs& a = p.a;
   const int warp = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31;
-  const int R = kTile * t + 32 * warp + lane;  // packed row of the unit
+  const int slot = kTile * t + 32 * warp + lane;         // the thread's row among the unit's slots
+  const int R = p.tile_rows * t + 32 * warp + lane;      // packed row of the unit
   const uint32_t lanes = (uint32_t)(32 * warp) << 16;
   const uint32_t tS = tmem + lanes + (uint32_t)(kTile * t);
   const uint32_t tO = tmem + lanes + (uint32_t)(2 * kTile + kTile * t);
@@ -501,7 +509,7 @@ FLINT_DEV void softmax_role(const Args& p, Ctl& C, uint8_t* smem, uint32_t tmem,
   for (uint32_t n = 0; piece_ready(C, n, a.status); ++n) {
     const Piece& u = C.piece[n % kPieces];
     const int nt = u.t1 - u.t0;
-    if (u.rows <= kTile * t) {  // the unit has one row tile
+    if (u.rows <= p.tile_rows * t) {  // the unit has one row tile
       n_tile += nt;
       piece_done(C, n);
       continue;
@@ -511,7 +519,7 @@ FLINT_DEV void softmax_role(const Args& p, Ctl& C, uint8_t* smem, uint32_t tmem,
     {
       const int G = a.nq / a.nkv, key0 = kTile * u.t0;
       int lim = u.keys - u.n + (u.r0 + R) / G - key0;  // last key that the row sees, from the tile's start
-      int lim0 = u.keys - u.n + (u.r0 + kTile * t + 32 * warp) / G - key0;  // the warp's first row
+      int lim0 = u.keys - u.n + (u.r0 + p.tile_rows * t + 32 * warp) / G - key0;  // the warp's first row
       for (int j = 0; j < nt; ++j, ++n_tile, lim -= kTile, lim0 -= kTile) {
         if (!wait(smem_addr(&C.s_full[t]), n_s & 1, C, a.status)) { ok = false; break; }
         ++n_s;
@@ -611,7 +619,7 @@ FLINT_DEV void softmax_role(const Args& p, Ctl& C, uint8_t* smem, uint32_t tmem,
       ++n_o;
       tc::fence_after_sync();
     }
-    const bool whole = u.c_first == u.c_last, valid = R < u.rows;
+    const bool whole = u.c_first == u.c_last, valid = 32 * warp + lane < p.tile_rows && R < u.rows;
     const long long row = out_row(a, u, R);
     uint16_t* dst = a.out + row * kHeadDim;
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;
@@ -630,7 +638,7 @@ FLINT_DEV void softmax_role(const Args& p, Ctl& C, uint8_t* smem, uint32_t tmem,
       } else {
 #pragma unroll
         for (int x = 0; x < 8; ++x)
-          *reinterpret_cast<uint4*>(part + ((size_t)(8 * i + x) * kUnitRows + R) * 4) =
+          *reinterpret_cast<uint4*>(part + ((size_t)(8 * i + x) * kUnitSlots + slot) * 4) =
               make_uint4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]);
       }
     }
@@ -642,8 +650,8 @@ FLINT_DEV void softmax_role(const Args& p, Ctl& C, uint8_t* smem, uint32_t tmem,
     if (whole) {
       if (valid && a.lse) a.lse[row] = finish_lse(m, l);
     } else {
-      part[kHeadDim * kUnitRows + R] = m;
-      part[(kHeadDim + 1) * kUnitRows + R] = l;
+      part[kHeadDim * kUnitSlots + slot] = m;
+      part[(kHeadDim + 1) * kUnitSlots + slot] = l;
       // the last of the unit's CTAs joins the parts
       __threadfence();
       __syncwarp();
@@ -664,7 +672,7 @@ FLINT_DEV void softmax_role(const Args& p, Ctl& C, uint8_t* smem, uint32_t tmem,
       ++n_wg;
       if (*reinterpret_cast<volatile int*>(&C.last[t])) {
         __threadfence();
-        join_row(p, u, R);
+        join_row(p, u, slot, R, valid);
       }
     }
     piece_done(C, n);
@@ -724,7 +732,7 @@ FLINT_DEV void mma_role(const Args& p, Ctl& C, uint8_t* smem, uint32_t tmem_any,
   };
   for (uint32_t n = 0; piece_ready(C, n, status); ++n) {
     const int nt = (int)uniform((uint32_t)(C.piece[n % kPieces].t1 - C.piece[n % kPieces].t0));
-    const bool both = uniform((uint32_t)C.piece[n % kPieces].rows) > kTile;
+    const bool both = uniform((uint32_t)C.piece[n % kPieces].rows) > (uint32_t)p.tile_rows;
     piece_done(C, n);
     if (nt == 0) continue;
     if (t == 1 && !both) {  // the unit has one row tile: the ring goes on without this one
@@ -795,8 +803,8 @@ FLINT_DEV void mma_role(const Args& p, Ctl& C, uint8_t* smem, uint32_t tmem_any,
 
 // ------------------------------------------------------------------ the loads
 // Q's rows, each row tile as soon as the last product with the previous
-// unit's is done: two tiled copies where G divides the tile (its rows are then
-// whole tokens), else 16-byte copies, 16 lanes per row.
+// unit's is done: two tiled copies (a row tile holds whole tokens), or 16-byte
+// copies, 16 lanes per row, for a group wider than the tile.
 FLINT_DEV void q_role(const Args& p, const Maps& maps, Ctl& C, uint8_t* smem) {
   const AttnArgs& a = p.a;
   const int lane = threadIdx.x & 31, hi = lane >> 4, ch = lane & 15, G = a.nq / a.nkv;
@@ -813,26 +821,27 @@ FLINT_DEV void q_role(const Args& p, const Maps& maps, Ctl& C, uint8_t* smem) {
     if (nt == 0) continue;
 #pragma unroll 1
     for (int t = 0; t < 2; ++t) {
-      if (rows <= kTile * t) break;
+      if (rows <= p.tile_rows * t) break;
       if (used[t] > 0 && !wait(smem_addr(&C.q_free[t]), (used[t] - 1) & 1, C, a.status)) break;
       ++used[t];
       if (p.q_tiled) {  // (rows past the unit's are other tokens', or zeros past T)
         if (lane == 0) {
-          bar_expect(smem_addr(&C.q_full[t]), kStageBytes);
+          bar_expect(smem_addr(&C.q_full[t]), (uint32_t)p.tile_rows * 256u);
           for (int half = 0; half < 2; ++half)
-            tc::tma_load_3d(smem + t * kStageBytes + half * kHalf, &maps.q, 64 * half, h * G, lo + (r0 + kTile * t) / G,
+            tc::tma_load_3d(smem + t * kStageBytes + half * kHalf, &maps.q, 64 * half, h * G, lo + (r0 + p.tile_rows * t) / G,
                             &C.q_full[t]);
         }
         __syncwarp();
         continue;
       }
-      const int q = r0 + kTile * t + hi, token = q / G;
+      const int q = r0 + p.tile_rows * t + hi, token = q / G;
       int head = q - token * G;
       const uint16_t* from = a.q + (long long)(lo + token) * a.q_stride + (long long)(h * G + head) * kHeadDim + 8 * ch;
       for (int i0 = 0; i0 < 64; i0 += 4) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const bool ok = kTile * t + 2 * (i0 + i) + hi < rows;
+          const int r = 2 * (i0 + i) + hi;
+          const bool ok = r < p.tile_rows && p.tile_rows * t + r < rows;
           cp_async16_or_zero(to[i] + (uint32_t)(t * kStageBytes + (i0 + i) * 256), ok ? from : a.q, ok);
           from += 2 * kHeadDim;  // two packed rows on
           head += 2;
@@ -1138,7 +1147,8 @@ PromptWs prompt_ws(void* base, int T, int B, int nq, int nkv) {
     off += (n + 255) / 256 * 256;
     return p;
   };
-  const size_t entries = (size_t)T * (nq / nkv) / kUnitRows + B;
+  const int G = nq / nkv;
+  const size_t entries = (size_t)T * G / (2 * tile_rows(G)) + B;
   PromptWs w;
   static_assert(kAttnPromptCounters + 2 * kPromptCtas * sizeof(int) <= kAttnData, "counters overlap");
   w.count = reinterpret_cast<int*>(b + kAttnPromptCounters);
@@ -1159,7 +1169,8 @@ cudaError_t launch_attn_prompt(const AttnArgs& a, const PromptWs& w, cudaStream_
   Maps maps = {};
   const bool tiled = p.box >= kAttnMinBox && attn_map(&maps.k, a, a.k, p.box) && attn_map(&maps.v, a, a.v, p.box);
   const int G = a.nq / a.nkv;
-  p.q_tiled = kTile % G == 0 && attn_q_map(&maps.q, a, G, kTile / G);
+  p.tile_rows = tile_rows(G);
+  p.q_tiled = G <= kTile && attn_q_map(&maps.q, a, G, kTile / G);
   int sms = 0;
   cudaError_t err = device_sms(&sms);
   if (err != cudaSuccess) return err;

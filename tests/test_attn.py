@@ -309,6 +309,9 @@ PROMPT = [
     ([300, 60], [300, 10], 8, 2, 4),
     ([200], [200], 16, 2, 2),
     ([333, 130], [100, 130], 8, 1, 12),
+    ([90, 5], [90, 3], 130, 1, 16),       # a group wider than a row tile
+    ([70], [70], 128, 1, 16),
+    ([140, 33], [140, 33], 48, 1, 16),
 ]
 
 
@@ -399,6 +402,18 @@ def test_prompt_same_bits_again_on_a_stream_and_pitched():
     other = fm.flint_attn_prompt(**g, stream=s)
     s.synchronize()
     assert torch.equal(out, other)
+
+
+@pytest.mark.gpu
+def test_prompt_with_one_query_row_for_all():
+    """q as a broadcast row (a pitch of 0): no tiled copies of it."""
+    p = Problem([150, 40], [150, 40], 16, 4, 16, seed=37)
+    p.q[:] = p.q[0]
+    g = p.gpu()
+    g["q"] = g["q"][:1].expand(190, -1)
+    lse = torch.empty(190, 16, dtype=torch.float32, device="cuda")
+    out = fm.flint_attn_prompt(**g, lse=lse)
+    check(out, lse, p.expect(SCALE, P_BF16), "one row")
 
 
 @pytest.mark.gpu
