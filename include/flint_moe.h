@@ -386,9 +386,12 @@ const char* flint_moe_strerror(int code);
  * 1..3 of the workspace, and every warp of the launch exits; the outputs of
  * such a call are undefined, the context stays usable and the next call
  * without the hook is exact again.  Nothing faults, traps or hangs.
+ * With site = FLINT_FAULT_ATTN_TURN the next flint_attn_prompt launches leave
+ * out the turn that the first row tile of a unit hands to the second: the
+ * waits give up in the same way, with FLINT_ERR_TIMEOUT in the status word.
  * site = 0 turns the hook off.  Returns FLINT_OK, or FLINT_ERR_INVALID_ARG
  * for an unknown site. */
-enum { FLINT_FAULT_NONE = 0, FLINT_FAULT_DOWN_HANDOVER = 17 };
+enum { FLINT_FAULT_NONE = 0, FLINT_FAULT_DOWN_HANDOVER = 17, FLINT_FAULT_ATTN_TURN = 18 };
 int flint_moe_debug_fault(int site);
 
 #ifdef __cplusplus

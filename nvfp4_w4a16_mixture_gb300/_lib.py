@@ -23,6 +23,7 @@ FLINT_ERR_TIMEOUT = -5
 FLINT_ERR_SCRATCH = -6
 FLINT_FAULT_NONE = 0
 FLINT_FAULT_DOWN_HANDOVER = 17
+FLINT_FAULT_ATTN_TURN = 18
 FLINT_PATH_NONE = 0
 FLINT_PATH_SINGLE_LAUNCH = 1
 FLINT_PATH_DECODE = 2

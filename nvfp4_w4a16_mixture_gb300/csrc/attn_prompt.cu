@@ -162,6 +162,7 @@ struct Args {
   int box, box_log2;  // rows of a tiled copy: gcd(block_size, 128)
   int tile_rows;      // rows of a row tile
   int q_tiled;        // whether maps.q is there
+  int fault;          // test hook: the first turn of a unit is left out
 };
 struct Maps {
   CUtensorMap k, v;  // {128, heads, slots, pages}, box {64, 1, box, 1}
@@ -315,6 +316,7 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const Args p, i
   pdl_wait();
   pdl_launch_dependents();
   __shared__ PlanShared S;
+  if (threadIdx.x < 2 * kPromptCtas) p.w.count[threadIdx.x] = 0;  // (whatever a call that gave up left)
   long long total = plan_pass<false>(p, S, false, 0, 0, 0);
   const bool loaded = p.a.B <= kPlanThreads;
   int least = 0;
@@ -662,7 +664,6 @@ FLINT_DEV void softmax_role(const Args& p, Ctl& C, uint8_t* smem, uint32_t tmem,
         __threadfence();
         int* cnt = p.w.count + 2 * u.c_first + t;
         const int last = atomicAdd(cnt, 1) == u.c_last - u.c_first;
-        if (last) *cnt = 0;
         C.last[t] = last;
         __threadfence();
       }
@@ -760,7 +761,7 @@ FLINT_DEV void mma_role(const Args& p, Ctl& C, uint8_t* smem, uint32_t tmem_any,
     opened = opened || both;
     tc::fence_after_sync();
     issue_s(uniform(st), nt == 1);
-    your_turn();
+    if (t == 1 || !p.fault) your_turn();
     next_stage();
     for (int j = 0; j < nt; ++j) {
       const bool more = j + 1 < nt;
@@ -1170,6 +1171,7 @@ cudaError_t launch_attn_prompt(const AttnArgs& a, const PromptWs& w, cudaStream_
   const bool tiled = p.box >= kAttnMinBox && attn_map(&maps.k, a, a.k, p.box) && attn_map(&maps.v, a, a.v, p.box);
   const int G = a.nq / a.nkv;
   p.tile_rows = tile_rows(G);
+  p.fault = debug_fault_site() == FLINT_FAULT_ATTN_TURN;
   p.q_tiled = G <= kTile && attn_q_map(&maps.q, a, G, kTile / G);
   int sms = 0;
   cudaError_t err = device_sms(&sms);

@@ -478,3 +478,86 @@ def test_decode_and_prompt_agree():
     want = p.expect(SCALE, P_BF16)
     check(a, la, want)
     check(b, lb, want)
+
+
+@pytest.mark.gpu
+def test_prompt_wait_that_runs_out():
+    """A turn that is never handed over: the waits give up after 200 ms, the
+    call is reported, and the next one on the same workspace is right again."""
+    p = Problem([300, 90], [300, 90], 16, 2, 16, seed=41)
+    g = p.gpu()
+    ws = torch.zeros(fm.flint_attn_prompt_workspace_bytes(390, 2, 16, 2), dtype=torch.uint8, device="cuda")
+    want = p.expect(SCALE, P_BF16)
+    fm.flint_moe_debug_fault(fm.FLINT_FAULT_ATTN_TURN)
+    try:
+        fm.flint_attn_prompt(**g, workspace=ws)
+        assert fm.flint_moe_status(ws) == fm.FLINT_ERR_TIMEOUT
+    finally:
+        fm.flint_moe_debug_fault(fm.FLINT_FAULT_NONE)
+    for _ in range(2):
+        out = fm.flint_attn_prompt(**g, workspace=ws)
+        assert fm.flint_moe_status(ws) == fm.FLINT_OK
+        check(out, None, want, "after the wait that ran out")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("prompt", [False, True])
+def test_output_on_any_16_bytes(prompt):
+    """Outputs that are aligned to 16 bytes and no more, and nothing beside them written."""
+    p = Problem([200, 45], [200, 45] if prompt else [1, 1], 16, 4, 16, seed=43)
+    g = p.gpu()
+    if not prompt:
+        g.pop("cu_q")
+    T = p.cu[-1]
+    buf = torch.full((T * 16 * D + 24,), 3.0, dtype=torch.bfloat16, device="cuda")
+    out = buf[8:8 + T * 16 * D].view(T, 16 * D)
+    (fm.flint_attn_prompt if prompt else fm.flint_attn_decode)(**g, out=out)
+    check(out, None, p.expect(SCALE, P_BF16 if prompt else P_SPLIT), "shifted")
+    assert bool((buf[:8] == 3.0).all()) and bool((buf[8 + T * 16 * D:] == 3.0).all())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("page", [16, 5])
+def test_pages_past_32_bits(page):
+    """Pages whose elements lie past 2^31 (a cache of 5 GB a side)."""
+    p = Problem([150, 40], [150, 40], 8, 4, page, seed=47)
+    g = p.gpu()
+    row = page * 4 * D
+    blocks = (1 << 31) // row + 3000
+    shift = blocks - p.blocks
+    k = torch.empty(blocks, page, 4, D, dtype=torch.bfloat16, device="cuda")
+    v = torch.empty_like(k)
+    k[shift:], v[shift:] = g["k_cache"], g["v_cache"]
+    table = torch.where((g["block_table"] >= 0) & (g["block_table"] < p.blocks), g["block_table"] + shift,
+                        g["block_table"])
+    g.update(k_cache=k, v_cache=v, block_table=table)
+    out = fm.flint_attn_prompt(**g)
+    check(out, None, p.expect(SCALE, P_BF16), "prompt")
+    g.pop("cu_q")
+    g["q"] = g["q"][[149, 189]].contiguous()
+    out = fm.flint_attn_decode(**g)
+    want = p.expect(SCALE, P_SPLIT)
+    check(out, None, tuple(w[[149, 189]] for w in want), "decode")
+    moves = torch.tensor([[blocks - 1, 5], [blocks - 2, blocks - p.blocks - 1]], dtype=torch.int32, device="cuda")
+    fm.flint_kv_copy_pages(k, v, moves)
+    for src, dst in moves.tolist():
+        assert torch.equal(k[src].view(torch.int16), k[dst].view(torch.int16))
+        assert torch.equal(v[src].view(torch.int16), v[dst].view(torch.int16))
+
+
+@pytest.mark.gpu
+def test_two_streams_at_once():
+    """Calls that overlap on two streams, each with a workspace of its own."""
+    p = Problem([3000, 700, 64], [1, 1, 1], 16, 4, 16, seed=53)
+    r = Problem([500, 260], [500, 260], 16, 4, 16, seed=54)
+    a, b = p.gpu(), r.gpu()
+    a.pop("cu_q")
+    x, y = torch.cuda.Stream(), torch.cuda.Stream()
+    for s in (x, y):
+        s.wait_stream(torch.cuda.current_stream())
+    outs = [(fm.flint_attn_decode(**a, stream=x), fm.flint_attn_prompt(**b, stream=y)) for _ in range(8)]
+    torch.cuda.synchronize()
+    wa, wb = p.expect(SCALE, P_SPLIT), r.expect(SCALE, P_BF16)
+    for da, pb in outs:
+        check(da, None, wa, "decode beside a prompt")
+        check(pb, None, wb, "prompt beside decode")
