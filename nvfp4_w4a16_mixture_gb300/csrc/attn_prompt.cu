@@ -74,7 +74,6 @@ constexpr int kPieceReaders = 15;          // all warps but the walking one
 constexpr int kTileWeight = 2, kUnitWeight = 7, kLeastWeight = 24;
 constexpr float kLazy = 8.0f;
 constexpr uint32_t kWaitNs = 200u * 1000 * 1000;
-constexpr uint32_t kSuspendNs = 50000;
 constexpr int kPartFloats = kUnitSlots * (kHeadDim + 2);
 
 // Rows of a row tile that are used: whole tokens where a token's group fits
@@ -120,9 +119,9 @@ FLINT_DEV bool bar_test(uint32_t bar, uint32_t parity) {
 FLINT_DEV bool bar_try(uint32_t bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
-      "{ .reg .pred p; mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2, %3; selp.u32 %0, 1, 0, p; }"
+      "{ .reg .pred p; mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
       : "=r"(ok)
-      : "r"(bar), "r"(parity), "r"(kSuspendNs)
+      : "r"(bar), "r"(parity)
       : "memory");
   return ok != 0;
 }
