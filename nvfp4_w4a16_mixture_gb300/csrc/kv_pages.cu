@@ -173,17 +173,22 @@ __global__ void __launch_bounds__(kPlanThreads) kv_mark_kernel(const KvPlanArgs 
     s_low = a.rank[live >> 5] + __popc(a.bits[live >> 5] & ((1u << (live & 31)) - 1u));
   __syncthreads();
   const int low = s_low;
-  for (int w = threadIdx.x; w < words; w += kPlanThreads) {
-    const int p0 = 32 * w, rank = a.rank[w];
-    const uint32_t bits = a.bits[w];
-    const uint32_t ge = p0 >= live ? ~0u : (live - p0 >= 32 ? 0u : ~0u << (live - p0));
-    for (uint32_t x = bits & ge; x; x &= x - 1u) {  // used, to be moved
-      const int i = __ffs(x) - 1;
-      a.moves[2 * (long long)(rank + __popc(bits & ((1u << i) - 1u)) - low)] = p0 + i;
-    }
-    for (uint32_t x = ~bits & ~ge; x; x &= x - 1u) {  // unused, to be filled
-      const int i = __ffs(x) - 1;
-      a.moves[2 * (long long)(p0 + i - rank - __popc(bits & ((1u << i) - 1u))) + 1] = p0 + i;
+  // A warp takes a word's pages at once, lane = page, so that its store fills
+  // whole lines: the ranks of neighbouring pages are neighbours in the list.
+  const int lane = threadIdx.x & 31;
+  const uint32_t lower = (1u << lane) - 1u;
+  for (int w0 = (int)threadIdx.x & ~31; w0 < words; w0 += kPlanThreads) {
+    const int n = min(32, words - w0);
+    const int ranks = lane < n ? a.rank[w0 + lane] : 0;
+    const uint32_t bitss = lane < n ? a.bits[w0 + lane] : 0u;
+#pragma unroll 4
+    for (int j = 0; j < n; ++j) {
+      const uint32_t bits = __shfl_sync(0xffffffffu, bitss, j);
+      const int used_below = __shfl_sync(0xffffffffu, ranks, j) + __popc(bits & lower);
+      const int p = 32 * (w0 + j) + lane;
+      const bool used = (bits >> lane) & 1u, high = p >= live;
+      // used, to be moved: a pair's first; unused, to be filled: its second
+      if (used == high && p < a.num_blocks) a.moves[2 * (long long)(high ? used_below - low : p - used_below) + !high] = p;
     }
   }
   if (threadIdx.x == 0) {
