@@ -197,27 +197,33 @@ FLINT_DEV Entry load_entry(const int4* p) {
   return e;
 }
 
-FLINT_DEV long long scan_cta64(long long v, long long* warps, long long* all) {
+// Sums over the CTA's threads below this one; the totals in *all.
+struct Sums {
+  long long as_is, least;
+};
+FLINT_DEV Sums scan_cta(Sums v, Sums* warps, Sums* all) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  long long x = v;
-#pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
-    const long long y = __shfl_up_sync(0xffffffffu, x, d);
-    if (lane >= d) x += y;
-  }
-  if (lane == 31) warps[warp] = x;
-  __syncthreads();
-  if (warp == 0) {
-    long long w = warps[lane];
+  auto scan_warp = [&](Sums x) {
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
-      const long long y = __shfl_up_sync(0xffffffffu, w, d);
-      if (lane >= d) w += y;
+      const long long y = __shfl_up_sync(0xffffffffu, x.as_is, d), z = __shfl_up_sync(0xffffffffu, x.least, d);
+      if (lane >= d) {
+        x.as_is += y;
+        x.least += z;
+      }
     }
-    warps[lane] = w;
-  }
+    return x;
+  };
+  const Sums x = scan_warp(v);
+  if (lane == 31) warps[warp] = x;
   __syncthreads();
-  const long long r = x - v + (warp ? warps[warp - 1] : 0);
+  if (warp == 0) warps[lane] = scan_warp(warps[lane]);
+  __syncthreads();
+  Sums r = {x.as_is - v.as_is, x.least - v.least};
+  if (warp) {
+    r.as_is += warps[warp - 1].as_is;
+    r.least += warps[warp - 1].least;
+  }
   *all = warps[31];
   __syncthreads();
   return r;
@@ -226,37 +232,47 @@ FLINT_DEV long long scan_cta64(long long v, long long* warps, long long* all) {
 // One CTA: the entries of all sequences, their weights' prefix sums, and the
 // first unit of each of the main kernel's CTAs.  The sequences' data pass
 // through shared memory, kPlanThreads at a time; an entry finds its sequence
-// there by bisection.  Its weights are summed first (once more with a least
-// weight where there is little work), then everything is written.
+// there by bisection.  The weights are summed first, both as they are and with
+// the least weight that holds where there is little work; then everything is
+// written.  Up to kPlanThreads sequences and entries the second pass takes
+// what the first one found (a scan of the CTA costs 0.4 us).
 constexpr int kPlanThreads = 1024;
 struct PlanShared {
   int lo[kPlanThreads], n[kPlanThreads], keys[kPlanThreads], first[kPlanThreads + 1];
-  long long scan[32];
+  Sums scan[32];
+};
+// What a thread keeps of the first pass: its (last) entry and the sums below it.
+struct PlanThread {
+  Entry x;
+  Sums at;
+  bool kept;
 };
 
-// Sum of the weights; with WRITE also the entries, prefixes and starts.
+// Sums of the weights; with WRITE also the entries, prefixes and starts.
 template <bool WRITE>
-FLINT_DEV long long plan_pass(const Args& p, PlanShared& S, bool loaded, int least, long long total, long long ctas) {
+FLINT_DEV Sums plan_pass(const Args& p, PlanShared& S, PlanThread& t, int least, long long total, long long ctas) {
   const AttnArgs& a = p.a;
   const int tid = threadIdx.x, G = a.nq / a.nkv;
   const int unit_rows = 2 * p.tile_rows;
   const long long most = (long long)a.T * G / unit_rows + a.B;  // entries that the table holds
-  long long sum = 0, e_base = 0;
+  const bool again = WRITE && t.kept;
+  Sums sum = {0, 0};
+  long long e_base = 0;
   for (int b0 = 0; b0 < a.B; b0 += kPlanThreads) {
     const int n_seq = min(kPlanThreads, a.B - b0);
-    if (!loaded) {
+    if (!again) {
       int lo = 0, n = 0, keys = 0;
       if (tid < n_seq) {
         keys = seq_keys(a, b0 + tid);
         seq_rows(a, b0 + tid, lo, n);
       }
-      long long all;
-      const long long at = scan_cta64(((long long)n * G + unit_rows - 1) / unit_rows, S.scan, &all);
+      Sums all;
+      const Sums at = scan_cta({((long long)n * G + unit_rows - 1) / unit_rows, 0}, S.scan, &all);
       S.lo[tid] = lo;
       S.n[tid] = n;
       S.keys[tid] = keys;
-      S.first[tid] = (int)at;
-      if (tid == 0) S.first[kPlanThreads] = (int)all;
+      S.first[tid] = (int)at.as_is;
+      if (tid == 0) S.first[kPlanThreads] = (int)all.as_is;
       __syncthreads();
     }
     // (overlapping pieces of a bad cu_q could outgrow the table: cut off there)
@@ -264,27 +280,36 @@ FLINT_DEV long long plan_pass(const Args& p, PlanShared& S, bool loaded, int lea
     if (here < S.first[kPlanThreads] && tid == 0) attn_error(a.status);
     for (long long e0 = 0; e0 < here; e0 += kPlanThreads) {
       const int e = (int)e0 + tid;
-      Entry x = {};
-      long long w = 0;
-      if (e < here) {
-        int i = 0;  // the last sequence whose first entry is at most e
-        for (int step = kPlanThreads / 2; step; step >>= 1)
-          if (i + step < n_seq && S.first[i + step] <= e) i += step;
-        x.b = b0 + i;
-        x.lo = S.lo[i];
-        x.n = S.n[i];
-        x.keys = S.keys[i];
-        x.r0 = (e - S.first[i]) * unit_rows;
-        x.rows = min(unit_rows, x.n * G - x.r0);
-        const int seen = max(0, min(x.keys, x.keys - x.n + (x.r0 + x.rows - 1) / G + 1));  // by its last row
-        x.tiles = (seen + kTile - 1) / kTile;
-        w = weight(x, least);
+      if (!again) {
+        Entry x = {};
+        Sums w = {0, 0};
+        if (e < here) {
+          int i = 0;  // the last sequence whose first entry is at most e
+          for (int step = kPlanThreads / 2; step; step >>= 1)
+            if (i + step < n_seq && S.first[i + step] <= e) i += step;
+          x.b = b0 + i;
+          x.lo = S.lo[i];
+          x.n = S.n[i];
+          x.keys = S.keys[i];
+          x.r0 = (e - S.first[i]) * unit_rows;
+          x.rows = min(unit_rows, x.n * G - x.r0);
+          const int seen = max(0, min(x.keys, x.keys - x.n + (x.r0 + x.rows - 1) / G + 1));  // by its last row
+          x.tiles = (seen + kTile - 1) / kTile;
+          w.as_is = (long long)weight(x, 0) * a.nkv;
+          w.least = (long long)weight(x, kLeastWeight) * a.nkv;
+        }
+        Sums all;
+        t.at = scan_cta(w, S.scan, &all);
+        t.x = x;
+        t.at.as_is += sum.as_is;
+        t.at.least += sum.least;
+        sum.as_is += all.as_is;
+        sum.least += all.least;
       }
-      long long all;
-      const long long at = sum + scan_cta64(w * a.nkv, S.scan, &all);
-      sum += all;
       if (WRITE && e < here) {
-        const long long i = e_base + e, end = at + w * a.nkv;
+        const Entry x = t.x;
+        const long long w = weight(x, least);
+        const long long i = e_base + e, at = least ? t.at.least : t.at.as_is, end = at + w * a.nkv;
         const int4 x0 = make_int4(x.b, x.lo, x.n, x.keys), x1 = make_int4(x.r0, x.rows, x.tiles, 0);
         p.w.entries[2 * i] = x0;
         p.w.entries[2 * i + 1] = x1;
@@ -307,6 +332,7 @@ FLINT_DEV long long plan_pass(const Args& p, PlanShared& S, bool loaded, int lea
     e_base += here;
     if (a.B > kPlanThreads) __syncthreads();  // before the next sequences take the place
   }
+  t.kept = a.B <= kPlanThreads && e_base <= kPlanThreads;
   return sum;
 }
 
@@ -316,17 +342,14 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const Args p, i
   pdl_launch_dependents();
   __shared__ PlanShared S;
   if (threadIdx.x < 2 * kPromptCtas) p.w.count[threadIdx.x] = 0;  // (whatever a call that gave up left)
-  long long total = plan_pass<false>(p, S, false, 0, 0, 0);
-  const bool loaded = p.a.B <= kPlanThreads;
-  int least = 0;
-  if (total / ctas < kLeastWeight) {
-    least = kLeastWeight;
-    total = plan_pass<false>(p, S, loaded, least, 0, 0);
-  }
+  PlanThread t = {};
+  const Sums sum = plan_pass<false>(p, S, t, 0, 0, 0);
+  const bool little = sum.as_is / ctas < kLeastWeight;
+  const long long total = little ? sum.least : sum.as_is;
   const long long n_cta = total == 0 ? 0 : max(1ll, min((long long)ctas, total / kLeastWeight));
   if ((int)threadIdx.x < ctas && (int)threadIdx.x >= n_cta)
     p.w.starts[kStartWords * threadIdx.x] = make_int4(0, 0, 0, 0);
-  if (total != 0) plan_pass<true>(p, S, loaded, least, total, n_cta);
+  if (total != 0) plan_pass<true>(p, S, t, little ? kLeastWeight : 0, total, n_cta);
 }
 
 // ------------------------------------------------------------- the pieces
