@@ -22,13 +22,13 @@
 //   warps 8, 9: MMA issue for row tile 0, 1, in turns.  Order S_0(0) S_1(0),
 //     then per j: PV_0(j) S_0(j+1) PV_1(j) S_1(j+1): while one tile's softmax
 //     runs, the other's products do;
-//   warps 10, 11, 14, 15: the key and value tiles (a ring of five 32 KB
+//   warps 10, 11, 14, 15: the key and value tiles (a ring of four 32 KB
 //     stages, K_0 V_0 K_1 V_1 ..) by tiled copies of a page's slots, or (tiny
 //     pages, strides that no tensor map takes) by 16-byte copies, which take
 //     the load-store unit's time from the barriers and cost 15 % more;
 //   warp 12: Q of the next unit; warp 13: walks along the CTA's work and
 //     publishes it to the others.
-// Shared memory: Q 2 x 32 KB, ring 5 x 32 KB.  TMEM: S_0, S_1, O_0, O_1, 128
+// Shared memory: Q 2 x 32 KB, ring 4 x 32 KB.  TMEM: S_0, S_1, O_0, O_1, 128
 // columns each.
 //
 // Work split: a plan kernel lays all units on a line by their weight (key
@@ -53,7 +53,7 @@ constexpr int kTile = 128;                 // rows of a row tile; keys of a key 
 constexpr int kUnitSlots = 2 * kTile;      // rows of a unit's parts in the workspace
 constexpr int kHalf = kTile * 128;         // 128 rows x 64 bf16
 constexpr int kStageBytes = 2 * kHalf;
-constexpr int kStages = 5;
+constexpr int kStages = 4;
 constexpr int kOffRing = 2 * kStageBytes;  // after Q_0, Q_1
 constexpr int kOffCtl = kOffRing + kStages * kStageBytes;
 // A warp runs on scheduler warp % 4: each has two of the softmax's, the MMA
@@ -69,9 +69,9 @@ constexpr int kInfo = 8;                   // key-tile records in flight
 constexpr int kPieces = 4;                 // pieces published ahead
 constexpr int kPieceReaders = 15;          // all warps but the walking one
 // Weights, in halves of a key tile's time (0.8 us): a unit's fixed part (Q,
-// first scores, output: about 5.5 us), and the least work worth a CTA of its
+// first scores, output: about 5 us), and the least work worth a CTA of its
 // own (a unit below it is not cut: joining its parts would cost 3 us and more).
-constexpr int kTileWeight = 2, kUnitWeight = 7, kLeastWeight = 24;
+constexpr int kTileWeight = 2, kUnitWeight = 6, kLeastWeight = 24;
 constexpr float kLazy = 8.0f;
 constexpr uint32_t kWaitNs = 200u * 1000 * 1000;
 constexpr int kPartFloats = kUnitSlots * (kHeadDim + 2);
@@ -972,7 +972,8 @@ FLINT_DEV void load_tiled_role(const Args& p, const Maps& maps, Ctl& C, uint8_t*
     }
   }
   if (aborted(C)) {  // no copy may land after the block has exited
-    for (uint32_t i = uses < 3u ? 0u : uses - 3u; i < uses; ++i) {
+    constexpr uint32_t kMost = (kStages + 1) / 2;  // of this warp's, on stages of their own
+    for (uint32_t i = uses < kMost ? 0u : uses - kMost; i < uses; ++i) {
       const uint32_t x = 2 * i + (uint32_t)kv, t = globaltimer_low();
       while (!bar_test(smem_addr(&C.full[x % kStages]), (x / kStages) & 1u) && globaltimer_low() - t < kWaitNs) {
       }
