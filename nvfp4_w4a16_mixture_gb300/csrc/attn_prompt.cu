@@ -36,6 +36,8 @@
 // CTA.  A unit cut by a border is shared: each CTA writes its part (O
 // unnormalised, m, l) to the workspace, and the one that finishes last joins
 // the parts in CTA order, so the result does not depend on which one that is.
+// Each warp's 32 rows are joined by themselves, and a part that finds the
+// others there is taken from TMEM.
 //
 // Keys past a sequence's end or on a page outside the cache: their scores
 // become -inf, and their rows in shared memory are zeros (whatever the slots
@@ -51,6 +53,7 @@ namespace {
 
 constexpr int kTile = 128;                 // rows of a row tile; keys of a key tile
 constexpr int kUnitSlots = 2 * kTile;      // rows of a unit's parts in the workspace
+constexpr int kGroups = kUnitSlots / 32;   // warps that a unit's rows are spread over
 constexpr int kHalf = kTile * 128;         // 128 rows x 64 bf16
 constexpr int kStageBytes = 2 * kHalf;
 constexpr int kStages = 4;
@@ -95,12 +98,11 @@ struct Piece {
 };
 struct Ctl {
   uint64_t full[kStages], empty[kStages];
-  uint64_t q_full[2], q_free[2], s_full[2], p_full[2][2], o_full[2], o_free[2], wg[2];
+  uint64_t q_full[2], q_free[2], s_full[2], p_full[2][2], o_full[2], o_free[2];
   uint64_t turn[2];  // row tile t may issue
   uint64_t piece_full[kPieces], piece_empty[kPieces];
   uint32_t tmem;
   int abort;
-  int last[2];
   TileInfo info[kInfo];
   Piece piece[kPieces];
 };
@@ -341,7 +343,7 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const Args p, i
   pdl_wait();
   pdl_launch_dependents();
   __shared__ PlanShared S;
-  if (threadIdx.x < 2 * kPromptCtas) p.w.count[threadIdx.x] = 0;  // (whatever a call that gave up left)
+  for (int i = threadIdx.x; i < kGroups * kPromptCtas; i += kPlanThreads) p.w.count[i] = 0;
   PlanThread t = {};
   const Sums sum = plan_pass<false>(p, S, t, 0, 0, 0);
   const bool little = sum.as_is / ctas < kLeastWeight;
@@ -484,38 +486,64 @@ FLINT_DEV float* part_of(const Args& p, const Piece& u, int cta) {
   return p.w.parts + (size_t)(2 * cta + (cta == u.c_first)) * kPartFloats;
 }
 
+// Finished parts of a row group (a warp's 32 rows) of a shared unit.
+FLINT_DEV int* parts_done(const Args& p, const Piece& u, int group) { return p.w.count + kGroups * u.c_first + group; }
+
 // The parts of a shared unit, joined in CTA order, for the row in slot `at`,
-// packed row R (if it is one of the unit's).
-FLINT_DEV void join_row(const Args& p, const Piece& u, int at, int R, bool valid) {
-  float m = neg_inf();
-  for (int x = u.c_first; x <= u.c_last; ++x) m = fmaxf(m, __ldcg(part_of(p, u, x) + kHeadDim * kUnitSlots + at));
-  float l = 0.0f;
-  float o[4][32];
+// packed row R (if it is one of the unit's).  This CTA's own part is still in
+// TMEM (at tO, if it saw any tile), with m_own and l_own.
+FLINT_DEV void join_row(const Args& p, const Piece& u, int at, int R, bool valid, uint32_t tO, bool any, float m_own,
+                        float l_own) {
+  const int own = blockIdx.x;
+  float m = m_own;
+  for (int x = u.c_first; x <= u.c_last; ++x)
+    if (x != own) m = fmaxf(m, __ldcg(part_of(p, u, x) + kHeadDim * kUnitSlots + at));
+  const long long row = out_row(p.a, u, R);
+  float l;
+#pragma unroll 1
+  for (int half = 0; half < 2; ++half) {
+    float o[2][32];
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < 64; ++i) o[i >> 5][i & 31] = 0.0f;
+    l = 0.0f;
+#pragma unroll 1
+    for (int x = u.c_first; x <= u.c_last; ++x) {
+      uint32_t v[2][32];
+      float pm = m_own, pl = l_own;
+      if (x != own) {
+        const float* pp = part_of(p, u, x);
+        const uint4* col = reinterpret_cast<const uint4*>(pp) + (size_t)(16 * half) * kUnitSlots + at;
 #pragma unroll
-    for (int x = 0; x < 32; ++x) o[i][x] = 0.0f;
-  for (int x = u.c_first; x <= u.c_last; ++x) {
-    const float* pp = part_of(p, u, x);
-    const float pm = __ldcg(pp + kHeadDim * kUnitSlots + at), pl = __ldcg(pp + (kHeadDim + 1) * kUnitSlots + at);
-    const float f = pm == neg_inf() ? (pl == 0.0f ? 0.0f : 1.0f) : ex2(pm - m);
-    l += f * pl;
+        for (int i = 0; i < 16; ++i) {
+          const uint4 q = __ldcg(col + (size_t)i * kUnitSlots);
+          v[i >> 3][4 * (i & 7)] = q.x;
+          v[i >> 3][4 * (i & 7) + 1] = q.y;
+          v[i >> 3][4 * (i & 7) + 2] = q.z;
+          v[i >> 3][4 * (i & 7) + 3] = q.w;
+        }
+        pm = __ldcg(pp + kHeadDim * kUnitSlots + at);
+        pl = __ldcg(pp + (kHeadDim + 1) * kUnitSlots + at);
+      } else if (any) {
 #pragma unroll
-    for (int i = 0; i < 32; ++i) {
-      const float4 v = __ldcg(reinterpret_cast<const float4*>(pp) + (size_t)i * kUnitSlots + at);
-      o[i >> 3][4 * (i & 7)] += f * v.x;
-      o[i >> 3][4 * (i & 7) + 1] += f * v.y;
-      o[i >> 3][4 * (i & 7) + 2] += f * v.z;
-      o[i >> 3][4 * (i & 7) + 3] += f * v.w;
+        for (int i = 0; i < 2; ++i) tc::tmem_ld32_async(tO + 64 * half + 32 * i, v[i]);
+        tc::tmem_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 2; ++i) tc::tmem_regs_ready(v[i]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 64; ++i) v[i >> 5][i & 31] = 0u;
+      }
+      const float f = pm == neg_inf() ? (pl == 0.0f ? 0.0f : 1.0f) : ex2(pm - m);
+      l += f * pl;
+#pragma unroll
+      for (int i = 0; i < 64; ++i) o[i >> 5][i & 31] += f * __uint_as_float(v[i >> 5][i & 31]);
     }
-  }
-  if (valid) {
-    const long long row = out_row(p.a, u, R);
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    if (valid)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) store_cols(p.a.out + row * kHeadDim + 32 * i, o[i], inv);
-    if (p.a.lse) p.a.lse[row] = finish_lse(m, l);
+      for (int i = 0; i < 2; ++i) store_cols(p.a.out + row * kHeadDim + 64 * half + 32 * i, o[i], inv);
   }
+  if (valid && p.a.lse) p.a.lse[row] = finish_lse(m, l);
 }
 
 template <bool TILED>
@@ -528,8 +556,8 @@ FLINT_DEV void softmax_role(const Args& p, Ctl& C, uint8_t* smem, uint32_t tmem,
   const uint32_t tS = tmem + lanes + (uint32_t)(kTile * t);
   const uint32_t tO = tmem + lanes + (uint32_t)(2 * kTile + kTile * t);
   const float c = a.scale * 1.4426950408889634f;
-  uint32_t n_s = 0, n_o = 0, n_wg = 0;  // phases done: s_full, o_full, wg
-  int n_tile = 0;                       // key tiles of the CTA so far
+  uint32_t n_s = 0, n_o = 0;  // phases done: s_full, o_full
+  int n_tile = 0;             // key tiles of the CTA so far
   for (uint32_t n = 0; piece_ready(C, n, a.status); ++n) {
     const Piece& u = C.piece[n % kPieces];
     const int nt = u.t1 - u.t0;
@@ -638,65 +666,61 @@ FLINT_DEV void softmax_role(const Args& p, Ctl& C, uint8_t* smem, uint32_t tmem,
       }
     }
     if (!ok) break;
+    const bool whole = u.c_first == u.c_last, valid = 32 * warp + lane < p.tile_rows && R < u.rows;
+    int* done = parts_done(p, u, 4 * t + warp);
+    const int others = u.c_last - u.c_first;
+    // whether the other parts are there already, so that this one need not
+    // leave the chip (asked while the last product runs)
+    bool last = !whole && __all_sync(0xffffffffu, ld_acquire(done) == others);
     if (nt > 0) {
       if (!wait(smem_addr(&C.o_full[t]), n_o & 1, C, a.status)) break;
       ++n_o;
       tc::fence_after_sync();
     }
-    const bool whole = u.c_first == u.c_last, valid = 32 * warp + lane < p.tile_rows && R < u.rows;
-    const long long row = out_row(a, u, R);
-    uint16_t* dst = a.out + row * kHeadDim;
-    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-    float* part = part_of(p, u, blockIdx.x);
+    if (!last) {
+      const long long row = out_row(a, u, R);
+      uint16_t* dst = a.out + row * kHeadDim;
+      const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+      float* part = part_of(p, u, blockIdx.x);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      uint32_t o[32];
-      if (nt > 0) {
-        tc::tmem_ld32(tO + 32 * i, o);
-      } else {
+      for (int i = 0; i < 4; ++i) {
+        uint32_t o[32];
+        if (nt > 0) {
+          tc::tmem_ld32(tO + 32 * i, o);
+        } else {
 #pragma unroll
-        for (int x = 0; x < 32; ++x) o[x] = 0;
+          for (int x = 0; x < 32; ++x) o[x] = 0;
+        }
+        if (whole) {
+          if (valid) store_cols(dst + 32 * i, reinterpret_cast<const float*>(o), inv);
+        } else {
+#pragma unroll
+          for (int x = 0; x < 8; ++x)
+            *reinterpret_cast<uint4*>(part + ((size_t)(8 * i + x) * kUnitSlots + slot) * 4) =
+                make_uint4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]);
+        }
       }
       if (whole) {
-        if (valid) store_cols(dst + 32 * i, reinterpret_cast<const float*>(o), inv);
+        if (valid && a.lse) a.lse[row] = finish_lse(m, l);
       } else {
-#pragma unroll
-        for (int x = 0; x < 8; ++x)
-          *reinterpret_cast<uint4*>(part + ((size_t)(8 * i + x) * kUnitSlots + slot) * 4) =
-              make_uint4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]);
+        part[kHeadDim * kUnitSlots + slot] = m;
+        part[(kHeadDim + 1) * kUnitSlots + slot] = l;
+        __syncwarp();
+        int n_done = 0;
+        if (lane == 0) {
+          __threadfence();
+          n_done = atomicAdd(done, 1);
+        }
+        last = __shfl_sync(0xffffffffu, n_done, 0) == others;
+        if (last) __threadfence();
       }
     }
+    // the last of the unit's CTAs joins the parts
+    if (last) join_row(p, u, slot, R, valid, tO, nt > 0, m, l);
     if (nt > 0) {
       tc::fence_before_sync();
       __syncwarp();
       if (lane == 0) bar_arrive(smem_addr(&C.o_free[t]));
-    }
-    if (whole) {
-      if (valid && a.lse) a.lse[row] = finish_lse(m, l);
-    } else {
-      part[kHeadDim * kUnitSlots + slot] = m;
-      part[(kHeadDim + 1) * kUnitSlots + slot] = l;
-      // the last of the unit's CTAs joins the parts
-      __threadfence();
-      __syncwarp();
-      if (lane == 0) bar_arrive(smem_addr(&C.wg[t]));
-      if (!wait(smem_addr(&C.wg[t]), n_wg & 1, C, a.status)) break;
-      ++n_wg;
-      if (warp == 0 && lane == 0) {
-        __threadfence();
-        int* cnt = p.w.count + 2 * u.c_first + t;
-        const int last = atomicAdd(cnt, 1) == u.c_last - u.c_first;
-        C.last[t] = last;
-        __threadfence();
-      }
-      __syncwarp();
-      if (lane == 0) bar_arrive(smem_addr(&C.wg[t]));
-      if (!wait(smem_addr(&C.wg[t]), n_wg & 1, C, a.status)) break;
-      ++n_wg;
-      if (*reinterpret_cast<volatile int*>(&C.last[t])) {
-        __threadfence();
-        join_row(p, u, slot, R, valid);
-      }
     }
     piece_done(C, n);
   }
@@ -1100,7 +1124,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&C.p_full[t][1], 4);
       mbar_init(&C.o_full[t], 1);
       mbar_init(&C.o_free[t], 4);
-      mbar_init(&C.wg[t], 4);
       mbar_init(&C.turn[t], 1);
     }
     C.abort = 0;
@@ -1174,7 +1197,7 @@ PromptWs prompt_ws(void* base, int T, int B, int nq, int nkv) {
   const int G = nq / nkv;
   const size_t entries = (size_t)T * G / (2 * tile_rows(G)) + B;
   PromptWs w;
-  static_assert(kAttnPromptCounters + 2 * kPromptCtas * sizeof(int) <= kAttnData, "counters overlap");
+  static_assert(kAttnPromptCounters + kGroups * kPromptCtas * sizeof(int) <= kAttnData, "counters overlap");
   w.count = reinterpret_cast<int*>(b + kAttnPromptCounters);
   w.parts = reinterpret_cast<float*>(take((size_t)2 * kPromptCtas * kPartFloats * sizeof(float)));
   w.starts = reinterpret_cast<int4*>(take(kPromptCtas * kStartWords * sizeof(int4)));

@@ -247,7 +247,7 @@ bool attn_q_map(CUtensorMap* m, const AttnArgs& a, int heads, int tokens);
 
 // Workspaces of both attention kernels: the status word, each kernel's
 // counters at a place of its own, then data.
-constexpr size_t kAttnRowsCounters = 256, kAttnPromptCounters = 1024, kAttnData = 4096;
+constexpr size_t kAttnRowsCounters = 256, kAttnPromptCounters = 1024, kAttnData = 8192;
 
 // Its work is cut into equal pieces, one per CTA; a unit that several CTAs
 // share is joined through the workspace.
@@ -264,7 +264,7 @@ cudaError_t launch_attn_rows(const AttnArgs& a, const RowsWs& w, cudaStream_t st
 // results of units that several CTAs share, in the workspace.
 constexpr int kPromptCtas = 152;  // most CTAs of its grid (one per SM)
 struct PromptWs {
-  int* count;            // [2 * kPromptCtas]: finished parts of a shared unit; the plan zeroes them
+  int* count;            // [8 * kPromptCtas]: finished parts of a shared unit's warps' rows; the plan zeroes them
   int4* starts;          // [kPromptCtas, 5]: where each CTA's piece begins
   int4* entries;         // [entries, 2]
   long long* prefix;     // [entries]: weight before each entry
