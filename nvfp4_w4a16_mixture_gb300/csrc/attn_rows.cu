@@ -29,7 +29,8 @@
 // lengths by one scan at the kernel's start.  A unit cut by a border is
 // shared: its CTAs write their parts (O unnormalised, m, l) to the workspace
 // and the one that finishes last joins them in CTA order, so the result does
-// not depend on which one that is.
+// not depend on which one that is.  Each warp does so for its own row, by a
+// count of its own, and a part that finds the others there stays on the chip.
 #include <cuda.h>
 
 #include "attn.cuh"
@@ -161,7 +162,6 @@ struct Parts {
   float m[kRowsWarps][8 * NT], l[kRowsWarps][8 * NT];
   uint64_t full[kRowsWarps][3];  // per warp and ring slot: the chunk's bytes are there
   int start[4];
-  int last;
   long long pos;
   long long scan[kRowsWarps];
 };
@@ -580,16 +580,25 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
         phase ^= 1u;
       }
     }
-    // ---- the unit's end in this CTA
+    // ---- the unit's end in this CTA, a warp per row (and the row 8 below)
     more = comp.template next<true>(a, coming);
     if (more) ask_q(coming);
+    const int others = u.c_last - u.c_first;  // CTAs that share the unit with this one
+    int* done = args.w.count + kRowsWarps * u.c_first + warp;
+    // whether the rows' other parts are there already, so that this one need
+    // not leave the chip (asked while the warps meet)
+    const int early = others && warp < u.rows ? ld_acquire(done) : -1;
     __syncthreads();  // all warps have taken Q
     store_part<NT>(P, A);
     __syncthreads();
-    const bool whole = u.c_first == u.c_last;
+    bool last = others && __all_sync(0xffffffffu, early == others);
     float* part = args.w.parts + (size_t)(2 * blockIdx.x + ((int)blockIdx.x == u.c_first)) * kPartFloats<NT>;
-    for (int i = threadIdx.x; i < u.rows * 32; i += kRowsThreads) {
-      const int r = i >> 5, d4 = i & 31;
+    float4 o_own[NT];
+    float m_own[NT], l_own[NT];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int r = warp + 8 * nt;
+      if (r >= u.rows) break;
       float m = neg_inf();
 #pragma unroll
       for (int w = 0; w < kRowsWarps; ++w) m = fmaxf(m, P.m[w][r]);
@@ -598,51 +607,57 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
 #pragma unroll
       for (int w = 0; w < kRowsWarps; ++w) {
         const float x = part_factor(P.m[w][r], P.l[w][r], m);
-        const float4 v = *reinterpret_cast<const float4*>(&P.o[w][r][4 * d4]);
+        const float4 v = *reinterpret_cast<const float4*>(&P.o[w][r][4 * lane]);
         l += x * P.l[w][r];
         o.x += x * v.x;
         o.y += x * v.y;
         o.z += x * v.z;
         o.w += x * v.w;
       }
-      if (whole) {
-        write_row(a, u, r, d4, o, m, l);
-      } else {
-        *reinterpret_cast<float4*>(part + r * kHeadDim + 4 * d4) = o;
-        if (d4 == 0) {
+      if (!others) {
+        write_row(a, u, r, lane, o, m, l);
+      } else if (!last) {
+        *reinterpret_cast<float4*>(part + r * kHeadDim + 4 * lane) = o;
+        if (lane == 0) {
           part[8 * NT * kHeadDim + r] = m;
           part[8 * NT * (kHeadDim + 1) + r] = l;
         }
       }
+      o_own[nt] = o;
+      m_own[nt] = m;
+      l_own[nt] = l;
     }
-    if (!whole) {
-      __threadfence();
-      __syncthreads();
-      if (threadIdx.x == 0) {
-        __threadfence();
-        int* cnt = args.w.count + u.c_first;
-        const int last = atomicAdd(cnt, 1) == u.c_last - u.c_first;
-        if (last) *cnt = 0;
-        P.last = last;
-        __threadfence();
+    if (others && warp < u.rows) {
+      if (!last) {
+        __syncwarp();
+        int n_done = 0;
+        if (lane == 0) {
+          __threadfence();
+          n_done = atomicAdd(done, 1);
+        }
+        last = __shfl_sync(0xffffffffu, n_done, 0) == others;
+        if (last) __threadfence();
       }
-      __syncthreads();
-      if (P.last) {
-        // a warp per row: the parts' references and sums one per lane, then
-        // their outputs, several loads under way
-        const int n = u.c_last - u.c_first + 1;
+      if (last) {
+        // the parts' references and sums one per lane, then their outputs,
+        // several loads under way
+        if (lane == 0) *done = 0;
+        const int n = others + 1, own = (int)blockIdx.x - u.c_first;
         auto part_at = [&](int i) {
           const int x = u.c_first + i;
           return args.w.parts + (size_t)(2 * x + (i == 0)) * kPartFloats<NT>;
         };
         constexpr int kMost = (kRowsCtas + 31) / 32;
-        for (int r = warp; r < u.rows; r += kRowsWarps) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          const int r = warp + 8 * nt;
+          if (r >= u.rows) break;
           float pm[kMost], pl[kMost], m = neg_inf();
 #pragma unroll
           for (int x = 0; x < kMost; ++x) {
             const int i = 32 * x + lane;
-            pm[x] = i < n ? __ldcg(part_at(i) + 8 * NT * kHeadDim + r) : neg_inf();
-            pl[x] = i < n ? __ldcg(part_at(i) + 8 * NT * (kHeadDim + 1) + r) : 0.0f;
+            pm[x] = i == own ? m_own[nt] : (i < n ? __ldcg(part_at(i) + 8 * NT * kHeadDim + r) : neg_inf());
+            pl[x] = i == own ? l_own[nt] : (i < n ? __ldcg(part_at(i) + 8 * NT * (kHeadDim + 1) + r) : 0.0f);
           }
 #pragma unroll
           for (int x = 0; x < kMost; ++x) m = fmaxf(m, pm[x]);
@@ -657,10 +672,14 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
             for (int i0 = 0; i0 < here; i0 += 16) {
               float4 v[16];
 #pragma unroll
-              for (int i = 0; i < 16; ++i)
-                v[i] = i0 + i < here
-                           ? __ldcg(reinterpret_cast<const float4*>(part_at(32 * x + i0 + i) + r * kHeadDim + 4 * lane))
-                           : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+              for (int i = 0; i < 16; ++i) {
+                const int at = 32 * x + i0 + i;
+                v[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                if (at == own)
+                  v[i] = o_own[nt];
+                else if (i0 + i < here)
+                  v[i] = __ldcg(reinterpret_cast<const float4*>(part_at(at) + r * kHeadDim + 4 * lane));
+              }
 #pragma unroll
               for (int i = 0; i < 16; ++i) {
                 const float f = __shfl_sync(0xffffffffu, y, i0 + i);
@@ -714,7 +733,7 @@ cudaError_t launch_nt(const AttnArgs& a, const RowsWs& w, const Maps& maps, int 
 }  // namespace
 
 RowsWs rows_ws(void* base) {
-  static_assert(kAttnRowsCounters + kRowsCtas * sizeof(int) <= kAttnPromptCounters, "counters overlap");
+  static_assert(kAttnRowsCounters + kRowsWarps * kRowsCtas * sizeof(int) <= kAttnPromptCounters, "counters overlap");
   uint8_t* b = static_cast<uint8_t*>(base);
   RowsWs w;
   w.count = reinterpret_cast<int*>(b + kAttnRowsCounters);
