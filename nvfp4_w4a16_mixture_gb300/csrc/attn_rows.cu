@@ -45,6 +45,11 @@ constexpr int kTileKeys = 16 * kRowsWarps;
 constexpr int kUnitWeight = 3;  // a unit's fixed part, in tiles: about 1.9 us, beside 0.65 us (few units) to 1.4 us for a tile
 constexpr int kChunkBytes = 16 * kHeadDim * 2 * 2;  // 16 keys' K and V
 constexpr float kLazy = 8.0f;
+// Parts joined at a time.  One CTA takes in 64 bytes a cycle, so many parts are
+// joined in two steps: a sequence of 32781 keys with 16 query heads to one kv
+// head, in 152 parts, takes 14.5 us instead of 40.8 with one step for all.
+constexpr int kJoin = 13;
+static_assert(kJoin * kJoin >= kRowsCtas && kJoin <= 32, "two steps have to do");
 
 constexpr uint32_t kWaitNs = 200u * 1000 * 1000;
 constexpr int kOPitch = kHeadDim + 4;  // floats; keeps the parts' stores off each other's banks
@@ -285,6 +290,47 @@ FLINT_DEV bool find_piece(const AttnArgs& a, Parts<NT>& P, Walk<NT>& k) {
 
 // TILED: the chunks by tiled copies; otherwise (tiny pages, strides that no
 // tensor map has) by 16-byte copies.
+// Row r of n <= kJoin parts, those of CTAs first, first + step, .., joined in
+// that order; part `own` is in o, m, l, which take the result.  The outputs'
+// loads are all under way before the references and sums, one per lane, come.
+template <int NT, class PartOf>
+FLINT_DEV void join_row(PartOf part_of, int first, int step, int n, int own, int r, float4& o, float& m, float& l) {
+  const int lane = threadIdx.x & 31;
+  float4 v[kJoin];
+#pragma unroll
+  for (int i = 0; i < kJoin; ++i) {
+    v[i] = o;
+    if (i < n && i != own)
+      v[i] = __ldcg(reinterpret_cast<const float4*>(part_of(first + i * step) + r * kHeadDim + 4 * lane));
+  }
+  float pm = neg_inf(), pl = 0.0f;
+  if (lane == own) {
+    pm = m;
+    pl = l;
+  } else if (lane < n) {
+    const float* p = part_of(first + lane * step) + r;
+    pm = __ldcg(p + 8 * NT * kHeadDim);
+    pl = __ldcg(p + 8 * NT * (kHeadDim + 1));
+  }
+  m = pm;
+#pragma unroll
+  for (int d = 16; d >= 1; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+  const float y = part_factor(pm, pl, m), yl = y * pl;
+  l = 0.0f;
+  o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+  for (int i = 0; i < kJoin; ++i) {
+    const float f = __shfl_sync(0xffffffffu, y, i);
+    l += __shfl_sync(0xffffffffu, yl, i);
+    if (i < n) {
+      o.x += f * v[i].x;
+      o.y += f * v[i].y;
+      o.z += f * v[i].z;
+      o.w += f * v[i].w;
+    }
+  }
+}
+
 template <int NT, bool TILED>
 __global__ void __launch_bounds__(kRowsThreads, 1)
     attn_rows_kernel(const __grid_constant__ Args args, const __grid_constant__ Maps maps) {
@@ -583,16 +629,22 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
     // ---- the unit's end in this CTA, a warp per row (and the row 8 below)
     more = comp.template next<true>(a, coming);
     if (more) ask_q(coming);
-    const int others = u.c_last - u.c_first;  // CTAs that share the unit with this one
-    int* done = args.w.count + kRowsWarps * u.c_first + warp;
-    // whether the rows' other parts are there already, so that this one need
+    // A shared unit's parts are joined kJoin at a time: those of a group of
+    // neighbouring CTAs by the group's last, then the groups' by their last.
+    const int cta = blockIdx.x, group = (cta - u.c_first) / kJoin, lead = u.c_first + kJoin * group;
+    const int groups = (u.c_last - u.c_first) / kJoin + 1, peers = min(kJoin - 1, u.c_last - lead);
+    const bool whole = u.c_first == u.c_last;
+    int* done = args.w.count + kRowsWarps * (2 * lead + (group == 0)) + warp;
+    // whether the group's other parts are there already, so that this one need
     // not leave the chip (asked while the warps meet)
-    const int early = others && warp < u.rows ? ld_acquire(done) : -1;
+    const int early = peers && warp < u.rows ? ld_acquire(done) : -1;
     __syncthreads();  // all warps have taken Q
     store_part<NT>(P, A);
     __syncthreads();
-    bool last = others && __all_sync(0xffffffffu, early == others);
-    float* part = args.w.parts + (size_t)(2 * blockIdx.x + ((int)blockIdx.x == u.c_first)) * kPartFloats<NT>;
+    bool last = peers && __all_sync(0xffffffffu, early == peers);
+    auto part_of = [&](int x) {
+      return args.w.parts + (size_t)(2 * x + (x == u.c_first)) * kPartFloats<NT>;
+    };
     float4 o_own[NT];
     float m_own[NT], l_own[NT];
 #pragma unroll
@@ -614,87 +666,62 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
         o.z += x * v.z;
         o.w += x * v.w;
       }
-      if (!others) {
-        write_row(a, u, r, lane, o, m, l);
-      } else if (!last) {
-        *reinterpret_cast<float4*>(part + r * kHeadDim + 4 * lane) = o;
-        if (lane == 0) {
-          part[8 * NT * kHeadDim + r] = m;
-          part[8 * NT * (kHeadDim + 1) + r] = l;
-        }
-      }
+      if (whole) write_row(a, u, r, lane, o, m, l);
       o_own[nt] = o;
       m_own[nt] = m;
       l_own[nt] = l;
     }
-    if (others && warp < u.rows) {
-      if (!last) {
-        __syncwarp();
-        int n_done = 0;
-        if (lane == 0) {
-          __threadfence();
-          n_done = atomicAdd(done, 1);
-        }
-        last = __shfl_sync(0xffffffffu, n_done, 0) == others;
-        if (last) __threadfence();
-      }
-      if (last) {
-        // the parts' references and sums one per lane, then their outputs,
-        // several loads under way
-        if (lane == 0) *done = 0;
-        const int n = others + 1, own = (int)blockIdx.x - u.c_first;
-        auto part_at = [&](int i) {
-          const int x = u.c_first + i;
-          return args.w.parts + (size_t)(2 * x + (i == 0)) * kPartFloats<NT>;
-        };
-        constexpr int kMost = (kRowsCtas + 31) / 32;
+    if (!whole && warp < u.rows) {
+      // this part, among the `n` from `first` on, `step` CTAs apart
+      int first = lead, step = 1, n = peers + 1, own = cta - lead, slot_cta = cta;
+#pragma unroll 1
+      for (int level = 0;; ++level) {
+        if (n > 1 && !last) {
+          float* part = part_of(slot_cta);
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          const int r = warp + 8 * nt;
-          if (r >= u.rows) break;
-          float pm[kMost], pl[kMost], m = neg_inf();
-#pragma unroll
-          for (int x = 0; x < kMost; ++x) {
-            const int i = 32 * x + lane;
-            pm[x] = i == own ? m_own[nt] : (i < n ? __ldcg(part_at(i) + 8 * NT * kHeadDim + r) : neg_inf());
-            pl[x] = i == own ? l_own[nt] : (i < n ? __ldcg(part_at(i) + 8 * NT * (kHeadDim + 1) + r) : 0.0f);
-          }
-#pragma unroll
-          for (int x = 0; x < kMost; ++x) m = fmaxf(m, pm[x]);
-#pragma unroll
-          for (int d = 16; d >= 1; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-          float l = 0.0f;
-          float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll
-          for (int x = 0; x < kMost; ++x) {
-            const float y = part_factor(pm[x], pl[x], m), yl = y * pl[x];
-            const int here = min(32, n - 32 * x);
-            for (int i0 = 0; i0 < here; i0 += 16) {
-              float4 v[16];
-#pragma unroll
-              for (int i = 0; i < 16; ++i) {
-                const int at = 32 * x + i0 + i;
-                v[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                if (at == own)
-                  v[i] = o_own[nt];
-                else if (i0 + i < here)
-                  v[i] = __ldcg(reinterpret_cast<const float4*>(part_at(at) + r * kHeadDim + 4 * lane));
-              }
-#pragma unroll
-              for (int i = 0; i < 16; ++i) {
-                const float f = __shfl_sync(0xffffffffu, y, i0 + i);
-                l += __shfl_sync(0xffffffffu, yl, i0 + i);
-                if (i0 + i < here) {
-                  o.x += f * v[i].x;
-                  o.y += f * v[i].y;
-                  o.z += f * v[i].z;
-                  o.w += f * v[i].w;
-                }
-              }
+          for (int nt = 0; nt < NT; ++nt) {
+            const int r = warp + 8 * nt;
+            if (r >= u.rows) break;
+            *reinterpret_cast<float4*>(part + r * kHeadDim + 4 * lane) = o_own[nt];
+            if (lane == 0) {
+              part[8 * NT * kHeadDim + r] = m_own[nt];
+              part[8 * NT * (kHeadDim + 1) + r] = l_own[nt];
             }
           }
-          write_row(a, u, r, lane, o, m, l);
+          __syncwarp();
+          int n_done = 0;
+          if (lane == 0) {
+            __threadfence();
+            n_done = atomicAdd(done, 1);
+          }
+          if (__shfl_sync(0xffffffffu, n_done, 0) != n - 1) break;
+          __threadfence();
         }
+        if (n > 1) {
+          if (lane == 0) *done = 0;
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            const int r = warp + 8 * nt;
+            if (r >= u.rows) break;
+            join_row<NT>(part_of, first, step, n, own, r, o_own[nt], m_own[nt], l_own[nt]);
+          }
+        }
+        if (level == 1 || groups == 1) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            const int r = warp + 8 * nt;
+            if (r >= u.rows) break;
+            write_row(a, u, r, lane, o_own[nt], m_own[nt], l_own[nt]);
+          }
+          break;
+        }
+        first = u.c_first;
+        step = kJoin;
+        n = groups;
+        own = group;
+        slot_cta = lead;
+        last = false;
+        done = args.w.count + kRowsWarps * (2 * kRowsCtas + u.c_first) + warp;
       }
     }
     __syncthreads();  // Parts is free again
@@ -733,7 +760,7 @@ cudaError_t launch_nt(const AttnArgs& a, const RowsWs& w, const Maps& maps, int 
 }  // namespace
 
 RowsWs rows_ws(void* base) {
-  static_assert(kAttnRowsCounters + kRowsWarps * kRowsCtas * sizeof(int) <= kAttnPromptCounters, "counters overlap");
+  static_assert(kAttnRowsCounters + 3 * kRowsWarps * kRowsCtas * sizeof(int) <= kAttnPromptCounters, "counters overlap");
   uint8_t* b = static_cast<uint8_t*>(base);
   RowsWs w;
   w.count = reinterpret_cast<int*>(b + kAttnRowsCounters);

@@ -247,13 +247,13 @@ bool attn_q_map(CUtensorMap* m, const AttnArgs& a, int heads, int tokens);
 
 // Workspaces of both attention kernels: the status word, each kernel's
 // counters at a place of its own, then data.
-constexpr size_t kAttnRowsCounters = 256, kAttnPromptCounters = 8192, kAttnData = 16384;
+constexpr size_t kAttnRowsCounters = 256, kAttnPromptCounters = 16384, kAttnData = 24576;
 
 // Its work is cut into equal pieces, one per CTA; a unit that several CTAs
 // share is joined through the workspace.
 constexpr int kRowsCtas = 152;  // most CTAs of its grid (one per SM)
 struct RowsWs {
-  int* count;    // [8 * kRowsCtas]: finished parts of a shared unit's rows, by warp; zero between calls
+  int* count;    // [3 * kRowsCtas, 8]: finished parts of groups' rows, by warp; zero between calls
   float* parts;  // [2 * kRowsCtas] slots
   size_t total;
 };

@@ -151,6 +151,20 @@ def test_decode_on_a_cache_with_shared_heads(nq):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("lens,nq,nkv", [([20000], 16, 1), ([20000, 3], 12, 2), ([9000], 32, 4), ([1790, 1700], 8, 1),
+                                         ([2300], 20, 2), ([1700], 8, 1)])
+def test_decode_units_in_many_parts(lens, nq, nkv):
+    """Units that 13 to 152 CTAs share, joined in one step or two; the same
+    bits each time, whichever part comes last."""
+    p = Problem(lens, [1] * len(lens), nq, nkv, 16, seed=nq)
+    out, lse = run_decode(p)
+    check(out, lse, p.expect(SCALE, P_SPLIT), f"decode {lens} {nq}/{nkv}")
+    for _ in range(5):
+        again = run_decode(p)
+        assert torch.equal(again[0], out) and torch.equal(again[1], lse)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("layout", LAYOUTS)
 def test_decode_layouts(layout):
     p = Problem([77, 300, 5], [1] * 3, 16, 4, 16, layout=layout, seed=5)
