@@ -78,8 +78,13 @@ int flint_attn_decode(const void* q, long long q_stride, const flint_kv_cache* c
  *   out    bf16 [T, num_q_heads * 128],  lse fp32 [T, num_q_heads] or NULL
  *   workspace  flint_attn_prompt_workspace_bytes(T, B, num_q_heads,
  *          num_kv_heads) bytes; it serves any T and B up to those.
- * The other arguments and the formula as for flint_attn_decode.  T = 0 and
- * B = 0 are no-ops. */
+ * The other arguments and the formula as for flint_attn_decode.  Scores,
+ * softmax sums and outputs are accumulated in fp32; the probabilities enter
+ * the second product as bf16.  A key that a row does not see does not reach
+ * its scores, sum or lse, whatever it holds; an infinite or NaN value of
+ * one of a sequence's own keys can make the outputs of rows up to 382 positions
+ * before it NaN as well (0 times it, within the tile).  What lies past a
+ * sequence's length reaches nothing.  T = 0 and B = 0 are no-ops. */
 size_t flint_attn_prompt_workspace_bytes(int T, int B, int num_q_heads, int num_kv_heads);
 int flint_attn_prompt(const void* q, long long q_stride, const flint_kv_cache* cache,
                       const int32_t* block_table, long long table_stride, int max_blocks, const int32_t* cu_q,

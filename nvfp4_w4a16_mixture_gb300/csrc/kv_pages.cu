@@ -4,13 +4,18 @@
 // Copy: bytes only.  A (pair, K or V, slot, head) row is 256 contiguous
 // bytes, 16 threads x 16 bytes; a CTA takes 64 rows of a pair's keys and
 // values at a time, eight 16-byte loads of each thread under way before the
-// first store, and asks for the next pair's page ids meanwhile.
+// first store, and asks for the next pair's page ids meanwhile.  8 CTAs an SM
+// share the items.  4360 pages of 16 slots and 4 heads: 46 us, 6.1 TB/s read
+// and written (a plain copy reaches 6.8); with 4 CTAs an SM 50, with a CTA per
+// item 60, with half the loads under way 47, with a quarter 56.
 // Plan: two kernels.  The first sets the bit of every page in use, and its
 // last CTA scans the bitmap: the live count, each word's number of live pages
 // below it, and the pairs; it leaves a copy of the bitmap for the second and
 // the bitmap itself cleared for the next call.  The second writes the new
 // table and fills up the list of pairs.  All in integers, so the result does
-// not depend on the order of the atomics.
+// not depend on the order of the atomics.  48 sequences in a pool of 24000
+// pages: 11 us, a chain of latencies (lengths and entries, atomics, the last
+// CTA's scan, its list, the second kernel's look-ups).
 #include "attn.cuh"
 
 namespace flint {
