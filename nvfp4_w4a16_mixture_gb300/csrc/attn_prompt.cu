@@ -29,7 +29,7 @@
 //     heads to 4: 69 us; tiled copies 46 with pages of 16, 52 with pages of 4);
 //   warp 12: Q of the next unit; warp 13: walks along the CTA's work and
 //     publishes it to the others.
-// Shared memory: Q 2 x 32 KB, ring 4 x 32 KB.  TMEM: S_0, S_1, O_0, O_1, 128
+// Shared memory: Q 3 x 32 KB, ring 4 x 32 KB.  TMEM: S_0, S_1, O_0, O_1, 128
 // columns each.
 //
 // Work split: a plan kernel lays all units on a line by their weight (key
@@ -47,14 +47,14 @@
 //
 // Measured (32 query heads to 4 unless given; rate of the useful products, of
 // 1873 TFLOP/s that a large bf16 product reaches): a prompt of 16384 tokens
-// 1300 us, 1692 TFLOP/s; 4096 tokens 110 us, 1254; 500 tokens after 30011
-// cached ones 170 us, 1462; 16 packed prompts of 1 to 2000 tokens, 8 kv heads,
-// 98 us, 627; one of 130 tokens 14.7 us, of which the plan takes 4.
+// 1305 us, 1685 TFLOP/s; 4096 tokens 110 us, 1250; 500 tokens after 30011
+// cached ones 172 us, 1441; 16 packed prompts of 1 to 2000 tokens, 8 kv heads,
+// 93 us, 664; one of 130 tokens 14.6 us, of which the plan takes 4.
 //   What bounds it: two row tiles and a key tile take 1.6 us, 3060 cycles of
 // which the tensor cores need 2048; the rest is the hand-overs between
 // products and softmax.  A unit costs 5 us more: until its first scores are
-// there nothing overlaps them (Q and two tiles of keys and values arrive at 64
-// bytes a cycle), and its output leaves at 32 bytes a cycle.  In a capture of
+// there nothing overlaps them (tiles arrive at 64 bytes a cycle), and its output
+// leaves at 32 bytes a cycle.  In a capture of
 // the 4096 tokens the tensor pipe is active 60 % of the time.
 #include <cuda.h>
 
@@ -70,7 +70,8 @@ constexpr int kGroups = kUnitSlots / 32;   // warps that a unit's rows are sprea
 constexpr int kHalf = kTile * 128;         // 128 rows x 64 bf16
 constexpr int kStageBytes = 2 * kHalf;
 constexpr int kStages = 4;                 // (16384 tokens: 3 take 27 % more, 5 no less)
-constexpr int kOffRing = 2 * kStageBytes;  // after Q_0, Q_1
+constexpr int kQs = 3;                     // places for row tiles' Q, taken in turn
+constexpr int kOffRing = kQs * kStageBytes;
 constexpr int kOffCtl = kOffRing + kStages * kStageBytes;
 // A warp runs on scheduler warp % 4: each has two of the softmax's, the MMA
 // warps share theirs with warps that seldom run, the loading ones have the
@@ -87,8 +88,8 @@ constexpr int kPieceReaders = 15;          // all warps but the walking one
 // Weights, in halves of a key tile's time (0.8 us): a unit's fixed part (Q,
 // first scores, output: about 5 us), and the least work worth a CTA of its
 // own (a unit below it is not cut: joining its parts would cost 3 us and more).
-// 16 packed prompts: a unit's weight of 5, 6, 7 gives 101, 98, 100 us; 4096
-// tokens 110, 110, 112; a least weight of 12 or 16 changes neither.
+// 16 packed prompts: a unit's weight of 4, 5, 6 gives 98, 96, 93 us, 4096 tokens
+// 112, 110, 110; a least weight of 12 or 16 changed neither.
 constexpr int kTileWeight = 2, kUnitWeight = 6, kLeastWeight = 24;
 constexpr float kLazy = 8.0f;
 constexpr uint32_t kWaitNs = 200u * 1000 * 1000;
@@ -113,7 +114,8 @@ struct Piece {
 };
 struct Ctl {
   uint64_t full[kStages], empty[kStages];
-  uint64_t q_full[2], q_free[2], s_full[2], p_full[2][2], o_full[2], o_free[2];
+  uint64_t q_full[kQs], q_free[kQs];
+  uint64_t s_full[2], p_full[2][2], o_full[2], o_free[2];
   uint64_t turn[2];  // row tile t may issue
   uint64_t piece_full[kPieces], piece_empty[kPieces];
   uint32_t tmem;
@@ -765,10 +767,11 @@ FLINT_DEV void mma_role(const Args& p, Ctl& C, uint8_t* smem, uint32_t tmem_any,
   // descriptors of the ring's first stage; a stage adds kStageBytes / 16 to
   // the low word (shared addresses stay below 2^18, inside its 14-bit field)
   const uint64_t dk0 = tc::desc_sw128(smem + kOffRing), dv0 = tc::desc_sw128_mn(smem + kOffRing, kHalf);
-  const uint32_t q_low = uniform((uint32_t)tc::desc_sw128(smem)) + t * (kStageBytes >> 4);
+  const uint32_t q_low = uniform((uint32_t)tc::desc_sw128(smem));
   const uint32_t k_low = uniform((uint32_t)dk0), v_low = uniform((uint32_t)dv0);
   uint32_t st = 0, ph = 0;                  // the next ring stage and its phase
   uint32_t n_unit = 0, n_p = 0, n_turn = 0;  // units, key tiles and turns so far
+  uint32_t q = 0, q_ph = 0;                 // place of the next unit's first Q and its phase
   bool opened = false;                       // whether there has been a unit of two row tiles
   auto next_stage = [&]() {
     if (++st == kStages) {
@@ -776,18 +779,18 @@ FLINT_DEV void mma_role(const Args& p, Ctl& C, uint8_t* smem, uint32_t tmem_any,
       ph ^= 1u;
     }
   };
-  // S_t = Q_t K^T, K in stage sk; whether it is Q_t's last use
-  auto issue_s = [&](uint32_t sk, bool last) {
+  // S_t = Q K^T: the descriptors' low words for Q, in place at, and K, in stage
+  // sk; whether it is Q's last use
+  auto issue_s = [&](uint32_t from, uint32_t low, uint32_t at, uint32_t sk, bool last) {
     if (elect()) {
-      const uint32_t low = k_low + sk * (kStageBytes >> 4);
 #pragma unroll
       for (int kk = 0; kk < 8; ++kk) {
         const uint32_t o = (uint32_t)((kk >> 2) * (kHalf >> 4) + 2 * (kk & 3));
-        tc::mma_bf16(tS, with_low(dk0, q_low + o), with_low(dk0, low + o), idS, kk > 0);
+        tc::mma_bf16(tS, with_low(dk0, from + o), with_low(dk0, low + o), idS, kk > 0);
       }
       bar_arrive(smem_addr(&C.s_full[t]));  // orders the tile's record before the softmax's reads
       bar_commit(smem_addr(&C.s_full[t]));
-      if (last) bar_commit(smem_addr(&C.q_free[t]));
+      if (last) bar_commit(smem_addr(&C.q_free[at]));
       bar_commit(smem_addr(&C.empty[sk]));
     }
     __syncwarp();
@@ -797,6 +800,21 @@ FLINT_DEV void mma_role(const Args& p, Ctl& C, uint8_t* smem, uint32_t tmem_any,
     const bool both = uniform((uint32_t)C.piece[n % kPieces].rows) > (uint32_t)p.tile_rows;
     piece_done(C, n);
     if (nt == 0) continue;
+    uint32_t at = q, at_ph = q_ph;  // this row tile's Q
+    auto next_q = [](uint32_t& i, uint32_t& parity) {
+      if (++i == kQs) {
+        i = 0;
+        parity ^= 1u;
+      }
+    };
+    next_q(q, q_ph);
+    if (both) {
+      if (t == 1) {
+        at = q;
+        at_ph = q_ph;
+      }
+      next_q(q, q_ph);
+    }
     if (t == 1 && !both) {  // the unit has one row tile: the ring goes on without this one
       for (int i = 0; i < 2 * nt; ++i) {
         if (!wait(smem_addr(&C.full[st]), ph, C, status)) return;
@@ -815,13 +833,13 @@ FLINT_DEV void mma_role(const Args& p, Ctl& C, uint8_t* smem, uint32_t tmem_any,
     };
     // ring order K_0 V_0 K_1 V_1 ..
     if (!wait(smem_addr(&C.full[st]), ph, C, status)) return;
-    if (!wait(smem_addr(&C.q_full[t]), n_unit & 1u, C, status)) return;
+    if (!wait(smem_addr(&C.q_full[at]), at_ph, C, status)) return;
     // (tile 0 opens a unit, once tile 1 has issued all of the last one: a turn
     // handed over twice before it is taken would be lost)
     if ((t == 1 || opened) && !my_turn()) return;
     opened = opened || both;
     tc::fence_after_sync();
-    issue_s(uniform(st), nt == 1);
+    issue_s(uniform(q_low + at * (kStageBytes >> 4)), uniform(k_low + st * (kStageBytes >> 4)), at, st, nt == 1);
     if (t == 1 || !p.fault) your_turn();
     next_stage();
     for (int j = 0; j < nt; ++j) {
@@ -830,6 +848,7 @@ FLINT_DEV void mma_role(const Args& p, Ctl& C, uint8_t* smem, uint32_t tmem_any,
       if (!wait(smem_addr(&C.full[sv]), ph, C, status)) return;
       next_stage();
       const uint32_t sk = uniform(st);
+      const uint32_t from = uniform(q_low + at * (kStageBytes >> 4)), low = uniform(k_low + st * (kStageBytes >> 4));
       if (more) {
         if (!wait(smem_addr(&C.full[sk]), ph, C, status)) return;
         next_stage();
@@ -856,7 +875,7 @@ FLINT_DEV void mma_role(const Args& p, Ctl& C, uint8_t* smem, uint32_t tmem_any,
         __syncwarp();
       }
       ++n_p;
-      if (more) issue_s(sk, j + 2 == nt);
+      if (more) issue_s(from, low, at, sk, j + 2 == nt);
       your_turn();
     }
     ++n_unit;
@@ -864,8 +883,9 @@ FLINT_DEV void mma_role(const Args& p, Ctl& C, uint8_t* smem, uint32_t tmem_any,
 }
 
 // ------------------------------------------------------------------ the loads
-// Q's rows, each row tile as soon as the last product with the previous
-// unit's is done: two tiled copies (a row tile holds whole tokens), or 16-byte
+// Q's rows, row tile after row tile, each as soon as its place is free (the
+// next unit's first one is on its way while this unit's two are in use; with
+// two places 16 packed prompts took 98 us instead of 93): two tiled copies (a row tile holds whole tokens), or 16-byte
 // copies, 16 lanes per row, for a group wider than the tile.
 FLINT_DEV void q_role(const Args& p, const Maps& maps, Ctl& C, uint8_t* smem) {
   const AttnArgs& a = p.a;
@@ -875,7 +895,7 @@ FLINT_DEV void q_role(const Args& p, const Maps& maps, Ctl& C, uint8_t* smem) {
   for (int q = 0; q < 4; ++q)
     to[q] = smem_addr(smem) + (uint32_t)((ch >> 3) * kHalf + hi * 128 + (((ch & 7) ^ ((2 * q + hi) & 7)) << 4));
   const long long wrap = a.q_stride - (long long)G * kHeadDim;  // from a token's group to the next token's
-  uint32_t used[2] = {0, 0};
+  uint32_t used = 0;  // places taken so far
   for (uint32_t n = 0; piece_ready(C, n, a.status); ++n) {
     const Piece& u = C.piece[n % kPieces];
     const int rows = u.rows, nt = u.t1 - u.t0, h = u.h, lo = u.lo, r0 = u.r0;
@@ -884,14 +904,15 @@ FLINT_DEV void q_role(const Args& p, const Maps& maps, Ctl& C, uint8_t* smem) {
 #pragma unroll 1
     for (int t = 0; t < 2; ++t) {
       if (rows <= p.tile_rows * t) break;
-      if (used[t] > 0 && !wait(smem_addr(&C.q_free[t]), (used[t] - 1) & 1, C, a.status)) break;
-      ++used[t];
+      const uint32_t at = used % kQs;
+      if (used >= (uint32_t)kQs && !wait(smem_addr(&C.q_free[at]), (used / kQs - 1) & 1, C, a.status)) break;
+      ++used;
       if (p.q_tiled) {  // (rows past the unit's are other tokens', or zeros past T)
         if (lane == 0) {
-          bar_expect(smem_addr(&C.q_full[t]), (uint32_t)p.tile_rows * 256u);
+          bar_expect(smem_addr(&C.q_full[at]), (uint32_t)p.tile_rows * 256u);
           for (int half = 0; half < 2; ++half)
-            tc::tma_load_3d(smem + t * kStageBytes + half * kHalf, &maps.q, 64 * half, h * G, lo + (r0 + p.tile_rows * t) / G,
-                            &C.q_full[t]);
+            tc::tma_load_3d(smem + at * kStageBytes + half * kHalf, &maps.q, 64 * half, h * G, lo + (r0 + p.tile_rows * t) / G,
+                            &C.q_full[at]);
         }
         __syncwarp();
         continue;
@@ -904,7 +925,7 @@ FLINT_DEV void q_role(const Args& p, const Maps& maps, Ctl& C, uint8_t* smem) {
         for (int i = 0; i < 4; ++i) {
           const int r = 2 * (i0 + i) + hi;
           const bool ok = r < p.tile_rows && p.tile_rows * t + r < rows;
-          cp_async16_or_zero(to[i] + (uint32_t)(t * kStageBytes + (i0 + i) * 256), ok ? from : a.q, ok);
+          cp_async16_or_zero(to[i] + (uint32_t)(at * kStageBytes + (i0 + i) * 256), ok ? from : a.q, ok);
           from += 2 * kHeadDim;  // two packed rows on
           head += 2;
           while (head >= G) {
@@ -917,13 +938,13 @@ FLINT_DEV void q_role(const Args& p, const Maps& maps, Ctl& C, uint8_t* smem) {
       cp_async_wait_all();
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) bar_arrive(smem_addr(&C.q_full[t]));
+      if (lane == 0) bar_arrive(smem_addr(&C.q_full[at]));
     }
   }
   if (p.q_tiled && aborted(C)) {  // no copy may land after the block has exited
-    for (int t = 0; t < 2; ++t) {
+    for (uint32_t i = used < (uint32_t)kQs ? 0u : used - kQs; i < used; ++i) {
       const uint32_t t0 = globaltimer_low();
-      while (used[t] > 0 && !bar_test(smem_addr(&C.q_full[t]), (used[t] - 1) & 1) && globaltimer_low() - t0 < kWaitNs) {
+      while (!bar_test(smem_addr(&C.q_full[i % kQs]), (i / kQs) & 1) && globaltimer_low() - t0 < kWaitNs) {
       }
     }
   }
@@ -1131,9 +1152,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&C.piece_full[i], 1);
       mbar_init(&C.piece_empty[i], kPieceReaders);
     }
+    for (int i = 0; i < kQs; ++i) {
+      mbar_init(&C.q_full[i], 1);
+      mbar_init(&C.q_free[i], 1);
+    }
     for (int t = 0; t < 2; ++t) {
-      mbar_init(&C.q_full[t], 1);
-      mbar_init(&C.q_free[t], 1);
       mbar_init(&C.s_full[t], 2);
       mbar_init(&C.p_full[t][0], 4);
       mbar_init(&C.p_full[t][1], 4);
