@@ -349,6 +349,17 @@ def test_prompt_many_units_of_one_and_two_row_tiles(longest, nq, nkv):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("count,longest,nq,nkv", [(1100, 4, 4, 2), (600, 80, 8, 1), (2100, 6, 64, 1), (1024, 2, 2, 2)])
+def test_prompt_plans_of_several_passes(count, longest, nq, nkv):
+    """More sequences, more units of work, or both than the plan's CTA has
+    threads; some sequences without rows or keys."""
+    n = [(7 * i * i + 3 * i) % (longest + 1) for i in range(count)]
+    p = Problem(n, n, nq, nkv, 16, seed=count)
+    out, lse = run_prompt(p)
+    check(out, lse, p.expect(SCALE, P_BF16), f"{count} prompts")
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("layout", LAYOUTS)
 def test_prompt_layouts(layout):
     p = Problem([177, 300, 5], [177, 140, 5], 16, 4, 16, layout=layout, seed=5)
