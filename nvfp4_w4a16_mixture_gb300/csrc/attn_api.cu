@@ -115,7 +115,7 @@ int flint_attn_prompt(const void* q, long long q_stride, const flint_kv_cache* c
                    num_q_heads, scale, out, lse, workspace, workspace_bytes, need, stream);
 }
 
-// Workspace: status word and a counter, one bit per page twice, the live pages
+// Workspace: the status word, one bit per page twice, the live pages
 // below each 32-page word.
 static size_t kv_words(long long num_blocks) { return ((size_t)num_blocks + 31) / 32; }
 static size_t kv_bits_bytes(long long num_blocks) { return (kv_words(num_blocks) * 4 + 255) / 256 * 256; }
@@ -180,7 +180,6 @@ int flint_kv_compact_plan(const int32_t* block_table, long long table_stride, in
   a.live = reinterpret_cast<uint32_t*>(wb + kStatusBytes);
   a.bits = reinterpret_cast<uint32_t*>(wb + kStatusBytes + kv_bits_bytes(num_blocks));
   a.rank = reinterpret_cast<int*>(wb + kStatusBytes + 2 * kv_bits_bytes(num_blocks));
-  a.done = reinterpret_cast<int*>(wb) + 16;
   a.status = reinterpret_cast<int*>(wb);
   return launch_kv_plan(a, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? FLINT_OK : FLINT_ERR_CUDA;
 }

@@ -300,9 +300,8 @@ struct KvPlanArgs {
   int* new_table;
   int* moves;
   int* counts;
-  int* done;       // workspace: CTAs that have marked, zero between calls
   uint32_t* live;  // workspace: one bit per page, all zero between calls
-  uint32_t* bits;  // workspace: their copy for the second kernel
+  uint32_t* bits;  // workspace: their copy for the renaming
   int* rank;       // workspace: live pages below each 32-page word
   int* status;
 };

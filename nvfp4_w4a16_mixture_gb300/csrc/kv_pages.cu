@@ -8,15 +8,17 @@
 // share the items.  4360 pages of 16 slots and 4 heads: 46 us, 6.1 TB/s read
 // and written (a plain copy reaches 6.8); with 4 CTAs an SM 50, with a CTA per
 // item 60, with half the loads under way 47, with a quarter 56.
-// Plan: two kernels.  The first sets the bit of every page in use, and its
-// last CTA scans the bitmap: the live count, each word's number of live pages
-// below it, and the pairs; it leaves a copy of the bitmap for the second and
-// the bitmap itself cleared for the next call.  The second writes the new
-// table and fills up the list of pairs.  All in integers, so the result does
-// not depend on the order of the atomics.  48 sequences in a pool of 24000
-// pages: 11 us, a chain of latencies (lengths and entries, atomics, the last
-// CTA's scan, its list, the second kernel's look-ups).
+// Plan: one cluster of 8 CTAs.  It sets the bit of every page in use, scans
+// the bitmap (the live count, each word's number of live pages below it), writes
+// the pairs, then the new table, and leaves the bitmap cleared for the next call.
+// All in integers, so the result does not depend on the order of the atomics.
+// It takes 5.5 us for a sequence of 8 pages, 10 us for 48 of up to 500 in a pool
+// of 24000 and 107 us for 256 of up to 2048 in one of 600000: a chain of
+// latencies (lengths and entries, atomics, the words, the list, look-ups).  Two
+// kernels over the whole GPU, of which the first's last CTA alone scanned and
+// wrote the list, took 6.5, 12 and 126 us; a cluster of 4 takes 6.0, 14 and 195.
 #include "attn.cuh"
+#include "tc.cuh"
 
 namespace flint {
 namespace {
@@ -126,110 +128,112 @@ FLINT_DEV int scan_cta(int v, int* warps, int* all) {
   return r;
 }
 
-// The used pages' bits; then, in the CTA that comes last, the ranks and pairs.
-__global__ void __launch_bounds__(kPlanThreads) kv_mark_kernel(const KvPlanArgs a) {
+// One cluster.  Phase 1: the used pages' bits, a warp per row or per part of
+// one, kEntries entries of each lane asked for together with the length.  Phase
+// 2: every CTA scans the whole bitmap and writes an eighth of the ranks and of
+// the list.  Phase 3: the same warps rename their entries.
+constexpr int kPlanCtas = 8, kEntries = 4;
+constexpr int kPlanWarps = kPlanCtas * kPlanThreads / 32;
+__global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads) kv_plan_kernel(const KvPlanArgs a) {
   SpanGuard<kSpanKvPlan> span_guard;
   pdl_wait();
   pdl_launch_dependents();
-  __shared__ int warps[32];
-  __shared__ int s_last;
-  for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
-    // (the first entries are asked for together with the length)
-    const int* row = a.block_table + (long long)b * a.table_stride;
-    int p = (int)threadIdx.x < a.max_blocks ? ldg_cg_i32(row + threadIdx.x) : 0;
-    const int used = seq_pages(a, ldg_cg_i32(a.seq_lens + b));
-    for (int i = threadIdx.x; i < used; i += kPlanThreads) {
-      if (i >= kPlanThreads) p = ldg_cg_i32(row + i);
-      if (p < 0 || p >= a.num_blocks)
-        attn_error(a.status);
-      else
-        atomicOr(a.live + (p >> 5), 1u << (p & 31));
+  __shared__ int scan[32], s_rank[kPlanThreads], s_low;
+  __shared__ uint32_t s_bits[kPlanThreads];
+  const int lane = threadIdx.x & 31, cta = blockIdx.x;
+  const int warp = (int)(threadIdx.x >> 5) * kPlanCtas + cta;  // (neighbouring rows on different CTAs)
+  const int parts = a.B > 0 ? max(1, kPlanWarps / a.B) : 1;    // warps of a row
+  constexpr int kChunk = 32 * kEntries;
+  if (threadIdx.x == 0) s_low = 0;
+
+  // f(index of the row's entry, the entry, entries in use) for all of this warp's
+  auto entries = [&](auto f) {
+    for (int item = warp; item < a.B * parts; item += kPlanWarps) {
+      const int b = item / parts;
+      const int* row = a.block_table + (long long)b * a.table_stride;
+      int used = -1;
+      for (int i0 = (item - b * parts) * kChunk; i0 < a.max_blocks; i0 += parts * kChunk) {
+        int p[kEntries];
+#pragma unroll
+        for (int x = 0; x < kEntries; ++x) {
+          const int i = i0 + 32 * x + lane;
+          p[x] = i < a.max_blocks ? ldg_cg_i32(row + i) : 0;
+        }
+        if (used < 0) used = seq_pages(a, ldg_cg_i32(a.seq_lens + b));
+#pragma unroll
+        for (int x = 0; x < kEntries; ++x) f(b, i0 + 32 * x + lane, p[x], used);
+      }
+      if (a.max_blocks == 0) seq_pages(a, ldg_cg_i32(a.seq_lens + b));  // (there is a length to check all the same)
     }
-  }
-  __threadfence();
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    const int last = atomicAdd(a.done, 1) == (int)gridDim.x - 1;
-    if (last) *a.done = 0;
-    s_last = last;
-    __threadfence();
-  }
-  __syncthreads();
-  if (!s_last) return;
+    __syncwarp();
+  };
+  entries([&](int, int i, int p, int used) {
+    if (i >= used) return;
+    if (p < 0 || p >= a.num_blocks)
+      attn_error(a.status);
+    else
+      atomicOr(a.live + (p >> 5), 1u << (p & 31));
+  });
+  tc::cluster_sync();
+
   const int words = (a.num_blocks + 31) / 32;
   int live = 0;
   for (int w0 = 0; w0 < words; w0 += kPlanThreads) {
     const int w = w0 + threadIdx.x;
     const uint32_t bits = w < words ? ldg_cg_u32(a.live + w) : 0u;
     int all;
-    const int below = scan_cta(__popc(bits), warps, &all);
-    if (w < words) {
-      a.rank[w] = live + below;
-      a.bits[w] = bits;
-      a.live[w] = 0u;
-    }
+    const int rank = live + scan_cta(__popc(bits), scan, &all);
     live += all;
-  }
-  // live pages below `live`: what its word's rank and lower bits say
-  __shared__ int s_low;
-  if (threadIdx.x == 0) s_low = live;  // (all pages are live)
-  __syncthreads();
-  if (live < a.num_blocks && (live >> 5) % kPlanThreads == (int)threadIdx.x)  // the thread that wrote that word
-    s_low = a.rank[live >> 5] + __popc(a.bits[live >> 5] & ((1u << (live & 31)) - 1u));
-  __syncthreads();
-  const int low = s_low;
-  // A warp takes a word's pages at once, lane = page, so that its store fills
-  // whole lines: the ranks of neighbouring pages are neighbours in the list.
-  const int lane = threadIdx.x & 31;
-  const uint32_t lower = (1u << lane) - 1u;
-  for (int w0 = (int)threadIdx.x & ~31; w0 < words; w0 += kPlanThreads) {
-    const int n = min(32, words - w0);
-    const int ranks = lane < n ? a.rank[w0 + lane] : 0;
-    const uint32_t bitss = lane < n ? a.bits[w0 + lane] : 0u;
-#pragma unroll 4
-    for (int j = 0; j < n; ++j) {
-      const uint32_t bits = __shfl_sync(0xffffffffu, bitss, j);
-      const int used_below = __shfl_sync(0xffffffffu, ranks, j) + __popc(bits & lower);
-      const int p = 32 * (w0 + j) + lane;
-      const bool used = (bits >> lane) & 1u, high = p >= live;
-      // used, to be moved: a pair's first; unused, to be filled: its second
-      if (used == high && p < a.num_blocks) a.moves[2 * (long long)(high ? used_below - low : p - used_below) + !high] = p;
+    if (w0 == 0) {
+      s_rank[threadIdx.x] = rank;
+      s_bits[threadIdx.x] = bits;
+    }
+    if (w < words && w % kPlanCtas == cta) {
+      a.rank[w] = rank;
+      a.bits[w] = bits;
     }
   }
-  if (threadIdx.x == 0) {
+  // used pages below `live`
+  int low = 0;
+  for (int w = threadIdx.x; 32 * (long long)w < live; w += kPlanThreads) {
+    const uint32_t bits = w < kPlanThreads ? s_bits[w] : ldg_cg_u32(a.live + w);
+    low += __popc(live - 32 * w >= 32 ? bits : bits & ((1u << (live - 32 * w)) - 1u));
+  }
+  low = __reduce_add_sync(0xffffffffu, low);
+  if (lane == 0 && low) atomicAdd(&s_low, low);
+  __syncthreads();
+  low = s_low;
+  // A warp takes a word's pages at once, lane = page: the ranks of neighbouring
+  // pages are neighbours in the list.
+#pragma unroll 4
+  for (int w = warp; w < words; w += kPlanWarps) {
+    const uint32_t bits = w < kPlanThreads ? s_bits[w] : a.bits[w];
+    const int used_below = (w < kPlanThreads ? s_rank[w] : a.rank[w]) + __popc(bits & ((1u << lane) - 1u));
+    const int p = 32 * w + lane;
+    const bool used = (bits >> lane) & 1u, high = p >= live;
+    // used, to be moved: a pair's first; unused, to be filled: its second
+    if (used == high && p < a.num_blocks) a.moves[2 * (long long)(high ? used_below - low : p - used_below) + !high] = p;
+  }
+  if (cta == 0 && threadIdx.x == 0) {
     a.counts[0] = live;
     a.counts[1] = live - low;
   }
-}
+  tc::cluster_sync();
 
-constexpr int kRenameThreads = 512;
-__global__ void __launch_bounds__(kRenameThreads) kv_rename_kernel(const KvPlanArgs a) {
-  SpanGuard<kSpanKvPlan> span_guard;
-  pdl_wait();
-  pdl_launch_dependents();
-  const int live = ldg_cg_i32(a.counts), above = ldg_cg_i32(a.counts + 1), low = live - above;
-  for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
-    const int* row = a.block_table + (long long)b * a.table_stride;
-    const int n = ldg_cg_i32(a.seq_lens + b);
-    int at = (int)threadIdx.x < a.max_blocks ? ldg_cg_i32(row + threadIdx.x) : 0;
-    const int used = seq_pages(a, n);
-    for (int i = threadIdx.x; i < a.max_blocks; i += kRenameThreads) {
-      int p = -1;
-      if (i < used) {
-        p = i < kRenameThreads ? at : ldg_cg_i32(row + i);
-        if (p < 0 || p >= a.num_blocks) {
-          p = -1;
-        } else if (p >= live) {
-          const int rank = ldg_cg_i32(a.rank + (p >> 5)) + __popc(ldg_cg_u32(a.bits + (p >> 5)) & ((1u << (p & 31)) - 1));
-          p = ldg_cg_i32(a.moves + 2 * (long long)(rank - low) + 1);
-        }
-      }
-      a.new_table[(long long)b * a.max_blocks + i] = p;
+  entries([&](int b, int i, int p, int used) {
+    if (i >= a.max_blocks) return;
+    if (i >= used || p < 0 || p >= a.num_blocks) {
+      p = -1;
+    } else if (p >= live) {
+      const int rank = ldg_cg_i32(a.rank + (p >> 5)) + __popc(ldg_cg_u32(a.bits + (p >> 5)) & ((1u << (p & 31)) - 1));
+      p = ldg_cg_i32(a.moves + 2 * (long long)(rank - low) + 1);
     }
-  }
-  const long long end = a.num_blocks / 2 * 2;  // (of the list's ints)
-  for (long long i = 2ll * above + blockIdx.x * kRenameThreads + threadIdx.x; i < end;
-       i += (long long)gridDim.x * kRenameThreads) a.moves[i] = -1;
+    a.new_table[(long long)b * a.max_blocks + i] = p;
+  });
+  const int thread = cta * kPlanThreads + threadIdx.x;
+  for (int w = thread; w < words; w += kPlanCtas * kPlanThreads) a.live[w] = 0u;  // for the next call
+  const long long end = a.num_blocks / 2 * 2;                                     // (of the list's ints)
+  for (long long i = 2ll * (live - low) + thread; i < end; i += kPlanCtas * kPlanThreads) a.moves[i] = -1;
 }
 
 template <class Args>
@@ -261,14 +265,7 @@ cudaError_t launch_kv_copy(const KvCopyArgs& a, cudaStream_t st) {
 }
 
 cudaError_t launch_kv_plan(const KvPlanArgs& a, cudaStream_t st) {
-  int sms = 0;
-  cudaError_t err = device_sms(&sms);
-  if (err != cudaSuccess) return err;
-  const int rows = a.B < 1 ? 1 : a.B;
-  err = launch_pdl(reinterpret_cast<const void*>(kv_mark_kernel), (unsigned)(rows < sms ? rows : sms), kPlanThreads, a, st);
-  if (err != cudaSuccess) return err;
-  return launch_pdl(reinterpret_cast<const void*>(kv_rename_kernel), (unsigned)(rows < 4 * sms ? rows : 4 * sms),
-                    kRenameThreads, a, st);
+  return launch_pdl(reinterpret_cast<const void*>(kv_plan_kernel), kPlanCtas, kPlanThreads, a, st);
 }
 
 FLINT_SPAN_SETTER(kv_pages)
