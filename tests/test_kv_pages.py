@@ -166,6 +166,37 @@ def test_compact_plan(blocks, page, lens, shared):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("rows", [255, 256, 257, 700])
+def test_compact_plan_many_rows(rows):
+    """As many rows as there are warps for them, and more."""
+    blocks, page = 9000, 4
+    lens = [(13 * i * i + i) % 45 for i in range(rows)]
+    need = [-(-n // page) for n in lens]
+    order = iter(torch.randperm(blocks, generator=torch.Generator().manual_seed(rows)).tolist())
+    table = [[next(order) for _ in range(n)] + [-1] * (12 - n) for n in need]
+    ws = torch.zeros(fm.flint_kv_workspace_bytes(blocks), dtype=torch.uint8, device="cuda")
+    new, moves, counts = fm.flint_kv_compact_plan(torch.tensor(table, dtype=torch.int32, device="cuda"),
+                                                  torch.tensor(lens, dtype=torch.int32, device="cuda"), page, blocks,
+                                                  workspace=ws)
+    assert fm.flint_moe_status(ws) == fm.FLINT_OK
+    want = plan(table, lens, page, blocks)
+    assert counts.tolist() == want[2] and new.tolist() == want[0]
+    assert np.array_equal(moves.cpu().numpy(), np.array(want[1], dtype=np.int32).reshape(-1, 2))
+
+
+@pytest.mark.gpu
+def test_compact_plan_without_columns():
+    """A table of no pages: lengths of 0 are right, others are reported."""
+    t = torch.empty(3, 0, dtype=torch.int32, device="cuda")
+    ws = torch.zeros(fm.flint_kv_workspace_bytes(10), dtype=torch.uint8, device="cuda")
+    for lens, status in (([0, 0, 0], fm.FLINT_OK), ([0, 2, 0], fm.FLINT_ERR_INVALID_ARG)):
+        n = torch.tensor(lens, dtype=torch.int32, device="cuda")
+        new, moves, counts = fm.flint_kv_compact_plan(t, n, 4, 10, workspace=ws)
+        assert fm.flint_moe_status(ws) == status
+        assert counts.tolist() == [0, 0] and (moves == -1).all() and new.shape == (3, 0)
+
+
+@pytest.mark.gpu
 def test_compact_plan_bad_pages():
     t = torch.tensor([[3, 99, 1], [-4, 5, 7]], dtype=torch.int32, device="cuda")
     n = torch.tensor([12, -1], dtype=torch.int32, device="cuda")
