@@ -23,7 +23,10 @@
  *                taken as 0 or as that bound, and the keys of a page outside
  *                [0, num_blocks) are left out; either records
  *                FLINT_ERR_INVALID_ARG.  Nothing outside the cache is read or
- *                written.
+ *                written.  A wait inside a kernel that runs out (200 ms) records
+ *                FLINT_ERR_TIMEOUT; the call ends, its outputs are not all
+ *                written, and the workspace serves the next call.  Calls that
+ *                may overlap (other streams) need workspaces of their own.
  */
 #ifndef FLINT_ATTN_H_
 #define FLINT_ATTN_H_
