@@ -47,10 +47,10 @@
 //
 // Measured (32 query heads to 4 unless given; rate of the useful products, of
 // 1873 TFLOP/s that a large bf16 product reaches): a prompt of 16384 tokens
-// 1305 us, 1685 TFLOP/s; 4096 tokens 110 us, 1250; 500 tokens after 30011
+// 1295 us, 1698 TFLOP/s; 4096 tokens 110 us, 1250; 500 tokens after 30011
 // cached ones 172 us, 1441; 16 packed prompts of 1 to 2000 tokens, 8 kv heads,
-// 93 us, 664; one of 130 tokens 14.6 us, of which the plan takes 4.
-//   What bounds it: two row tiles and a key tile take 1.6 us, 3060 cycles of
+// 94 us, 658; one of 130 tokens 14.6 us, of which the plan takes 4.
+//   What bounds it: two row tiles and a key tile take 1.6 us, 2960 cycles of
 // which the tensor cores need 2048; the rest is the hand-overs between
 // products and softmax.  A unit costs 5 us more: until its first scores are
 // there nothing overlaps them (tiles arrive at 64 bytes a cycle), and its output
@@ -855,8 +855,8 @@ FLINT_DEV void mma_role(const Args& p, Ctl& C, uint8_t* smem, uint32_t tmem_any,
       }
       // O_t of the CTA's previous unit has been read
       if (j == 0 && n_unit > 0 && !wait(smem_addr(&C.o_free[t]), (n_unit - 1) & 1u, C, status)) return;
-      if (!wait(smem_addr(&C.p_full[t][0]), n_p & 1u, C, status)) return;
       if (!my_turn()) return;
+      if (!wait(smem_addr(&C.p_full[t][0]), n_p & 1u, C, status)) return;
 #pragma unroll
       for (int half = 0; half < 2; ++half) {  // keys 0 .. 63, 64 .. 127
         if (half == 1 && !wait(smem_addr(&C.p_full[t][1]), n_p & 1u, C, status)) return;
